@@ -56,7 +56,11 @@ typedef enum {
 
 typedef enum { SAFE_BOOL = 0, SAFE_U8 = 1, SAFE_F32 = 2, SAFE_F16 = 3, SAFE_BF16 = 4 } safe_dtype;
 
-/* ABI version of this header (bumped on any signature or entry-point change): 7. */
+/* Formats of a microscaled matrix (see safe_mx_quantize). */
+typedef enum { SAFE_MXFP8 = 0, SAFE_MXFP4 = 1, SAFE_NVFP4 = 2 } safe_mx_format;
+
+/* ABI version of this header: 7. It changes when the signature or the meaning
+ * of an entry point does; entry points that are only added leave it. */
 int safe_abi_version(void);
 const char* safe_status_string(int status);
 
@@ -343,6 +347,130 @@ safe_status safe_sw_cfg(const void* f_c, const void* f_u, const float* s, void* 
 size_t safe_gather_linear_workspace_bytes(int B, int k, int d_in);
 safe_status safe_gather_linear(const void* X, const int32_t* S, int k, const void* Wt, const float* bias, int act,
                                void* Y, int B, int N, int d_in, int d_out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Root-mean-square norm of rows with the residual's addition: what lies
+ * between the branches of the block B (Eq. (18)) and of its row-selective
+ * form B^S (Eq. (15)). For every output row (b, r):
+ *   h = x + res            (res == NULL: h = x)
+ *   y = h / sqrt(mean(h^2) + eps) * w
+ * S == NULL: R = N rows in order, k ignored. Else R = k, row r belongs to
+ * token S[b, r]: res is read at that token, x at row r (x_full = 0) or at the
+ * token (x_full = 1).
+ *  x      device [B, R, D], or [B, N, D] with x_full = 1 (needs S).
+ *  res    device [B, N, D] (the residual stream) or NULL.
+ *  S      device int32 [B, k] or NULL. An index outside [0, N) is flagged
+ *         and its rows of h, y and q are zeros.
+ *  w      device fp32 [D] or NULL (ones).
+ *  h      device [B, R, D] (written) or NULL. h_full = 1 (with S, h == res):
+ *         the rows S of the stream are updated in place and every other row
+ *         is left as it is; S must then be strictly ascending (a row out of
+ *         order is flagged, leaves the stream as it is and its y is zero).
+ *  y      device [B, R, D] (written) or NULL.
+ *  q, q_scales  device, 16-byte aligned: y as SAFE_MXFP8 matrix of B * R rows
+ *         (layout and sizes: safe_mx_quantize), quantised from the fp32 y
+ *         without a rounding in between; both or neither. y or q, or both.
+ *  dtype  SAFE_F32 / SAFE_F16 / SAFE_BF16 of x, res, h and y.
+ * Tensors are contiguous and naturally aligned; 16-byte alignment of all of
+ * them with D a multiple of 8 is faster, and with q it is required, with D a
+ * multiple of 32 and at most 40960. Outputs may not overlap each other or an
+ * input, except that without S h and y may each be x or res themselves. All
+ * arithmetic is fp32: the norm takes the unrounded sum h.
+ */
+safe_status safe_rms_norm(const void* x, int x_full, const void* res, const int32_t* S, int k, const float* w,
+                          float eps, void* h, int h_full, void* y, void* q, void* q_scales, int dtype, int B, int N,
+                          int D, void* stream);
+
+/*
+ * Rotary positions of queries and keys. Pair i < r / 2 of every head turns by
+ * the angle pos * f_i; elements r .. d - 1 of a head pass through:
+ *   (a, b) -> m (a cos - b sin, b cos + a sin)
+ * with (a, b) = elements (i, i + r/2), or (2i, 2i + 1) when interleaved.
+ *  q, k   device [B, R, H, d] with element strides {sample, row, head} in
+ *         *_strides (host, >= 0; the head dim is contiguous), so views of a
+ *         fused q, k, v projection are taken as they are. k may be NULL (then
+ *         ok NULL, Hk 0). Hq and Hk need not be equal.
+ *  oq, ok device, the results, with strides of their own. Each is its input
+ *         itself (same strides: in place) or shares no element with the
+ *         inputs, and none with the other output or within itself: tensors
+ *         apart, or views side by side in the rows of one fused tensor (other
+ *         interleavings are refused).
+ *  dtype  SAFE_F32 / SAFE_F16 / SAFE_BF16.
+ *  freq   device int64 [r / 2]: f_i / (2 pi) in units of 2^-64 turns (modulo
+ *         one turn). pos * freq modulo 2^64 is the exact phase, at any
+ *         position.
+ *  sections  host int32 [axes], axes 1 .. 3: pairs of each position axis
+ *         in order, their sum is r / 2 (a latent grid has two axes).
+ *  pos    device int32 [N, axes] (pos_batched = 0, shared by the samples) or
+ *         [B, N, axes] (1); any value. NULL (axes = 1): the token index.
+ *  S      device int32 [B, R] tokens of the rows, or NULL (R == N, token r).
+ *         An index outside [0, N) is flagged and replaced by token 0.
+ *  m      factor on the rotated elements (1 for plain rotary positions).
+ * 2 <= r <= d <= 1024, r even. fp32 arithmetic, one rounding at the end.
+ */
+safe_status safe_rope(const void* q, const int64_t q_strides[3], void* oq, const int64_t oq_strides[3], int Hq,
+                      const void* k, const int64_t k_strides[3], void* ok, const int64_t ok_strides[3], int Hk,
+                      int dtype, const int64_t* freq, const int32_t* sections, int axes, const int32_t* pos,
+                      int pos_batched, const int32_t* S, int B, int N, int R, int d, int r, int interleaved, float m,
+                      void* stream);
+
+/*
+ * Microscaled rows. A matrix [rows, D] (D a multiple of 32) keeps one scale for
+ * each block of consecutive elements of a row:
+ *   SAFE_MXFP8  e4m3 elements, blocks of 32, power-of-two scales (e8m0)
+ *   SAFE_MXFP4  e2m1 elements, blocks of 32, power-of-two scales (e8m0)
+ *   SAFE_NVFP4  e2m1 elements, blocks of 16, e4m3 scales, and one factor g for
+ *               the whole matrix, in [2^-100, 2^100] (the others: g == 1)
+ * An element stands for element * scale * g. In memory:
+ *   data    row-major, D bytes (mxfp8) or D / 2 bytes (4 bits: the even
+ *           element in the low half) a row.
+ *   scales  safe_mx_scale_bytes(rows, D, fmt) bytes: tiles of 128 rows x 4
+ *           scales (512 bytes), those of the same 128 rows one after the
+ *           other; row i and scale j of a tile at byte
+ *           (i % 32) * 16 + (i / 32) * 4 + j. Scales that only fill tiles up
+ *           must be finite (safe_mx_quantize and safe_rms_norm write zeros).
+ *
+ * safe_mx_quantize: rows of X, those of S or all, into that form. With a the
+ * largest magnitude of a block: power-of-two scales have the exponent
+ * floor(log2 a) - 8 (mxfp8) or - 2 (mxfp4) (a = 0: 2^-127), so elements at the
+ * top of a block may saturate; nvfp4 scales are a / (6 g) rounded to e4m3 (at
+ * most 448). Elements are x / (scale g), and saturate at the largest finite
+ * value. Every rounding is to nearest, ties to even, of the exact quotient. A
+ * block that holds an infinity or a NaN gets a NaN scale.
+ *  X      device [B, N, D], dtype SAFE_F32 / SAFE_F16 / SAFE_BF16.
+ *  S      device int32 [B, k], any order (an index outside [0, N) is flagged
+ *         and replaced by row 0), or NULL: every row (k ignored).
+ *  data, scales  device, of B * (k or N) rows (written); apart from X and
+ *         from each other. X, data and scales are 16-byte aligned.
+ * safe_mx_dequantize: the values of `rows` rows, rounded to Y's dtype (Y
+ * device [rows, D], 16-byte aligned).
+ * safe_mx_scale_bytes returns 0 for sizes that have no such form.
+ */
+size_t safe_mx_scale_bytes(int64_t rows, int D, int fmt);
+safe_status safe_mx_quantize(const void* X, int dtype, const int32_t* S, int k, int fmt, float g, void* data,
+                             void* scales, int B, int N, int D, void* stream);
+safe_status safe_mx_dequantize(const void* data, const void* scales, int fmt, float g, void* Y, int dtype,
+                               int64_t rows, int D, void* stream);
+
+/*
+ * A row-wise layer (as safe_gather_linear) with both operands microscaled, in
+ * the same format:
+ *   Y[r, :] = act( alpha * sum_c X[r, c] W[:, c] + bias )
+ * where X and W stand for element * scale, and alpha is the product of their
+ * factors g (a normal fp32 number). The tensor cores multiply the 8- or 4-bit elements, apply both
+ * block scales and add in fp32; the result is rounded to bf16.
+ *  X, X_scales    device: rows x d_in (e.g. from safe_mx_quantize with the
+ *                 rows S, or from safe_rms_norm).
+ *  Wt, Wt_scales  device: d_out x d_in.
+ *  bias  device fp32 [d_out] (4-byte aligned) or NULL; act as
+ *        safe_gather_linear (0 = none, 1 = tanh-GELU).
+ *  Y     device bf16 [rows, d_out] (written; apart from the operands).
+ *  d_in >= 64 a multiple of 32, d_out >= 8 a multiple of 8; all pointers but
+ *  bias 16-byte aligned.
+ */
+safe_status safe_mx_linear(const void* X, const void* X_scales, const void* Wt, const void* Wt_scales, int fmt,
+                           float alpha, const float* bias, int act, void* Y, int64_t rows, int d_in, int d_out,
+                           void* stream);
 
 /*
  * Device status word: synchronises `stream`, writes to *h_status (host) the

@@ -18,6 +18,10 @@
 #include "aux_kernels.cuh"
 #include "guidance.cuh"
 #include "linear.cuh"
+#include "mx_quant.cuh"
+#include "norm.cuh"
+#include "rope.cuh"
+#include "mx_linear.cuh"
 
 using namespace safe;
 
@@ -424,6 +428,209 @@ bool srsu_compact_q(const void*& Q, int& q_compact, const int32_t* S, int k, int
   return true;
 }
 
+// ---------------------------------------------------------------- norm, positions, microscaled layers
+// Bytes of a floating type, 0 for the others.
+size_t float_size(int dtype) {
+  return dtype == SAFE_F32 ? 4 : dtype == SAFE_F16 || dtype == SAFE_BF16 ? 2 : 0;
+}
+bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+// Whether two ranges of memory share a byte (a null one shares none).
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && an > 0 && bn > 0 && x < y + bn && y < x + an;
+}
+// A strided [B, R, H, d] tensor (strides in elements, the head dim contiguous).
+struct View4 {
+  uintptr_t at;
+  int64_t size[3], stride[3];  // sample, row, head
+  int d;
+};
+// Whether blocks of `block` elements at the given strides share no element; dims
+// of one entry do not count. Covers the layouts in which each dim's stride
+// passes over all of the dims inside it.
+bool nested(int64_t block, const int64_t* size, const int64_t* stride, int n) {
+  bool used[3] = {};
+  for (int i = 0; i < n; ++i) {
+    int m = -1;
+    for (int j = 0; j < n; ++j)
+      if (!used[j] && size[j] > 1 && (m < 0 || stride[j] < stride[m])) m = j;
+    if (m < 0) return true;
+    if (stride[m] < block) return false;
+    block += (size[m] - 1) * stride[m];
+    used[m] = true;
+  }
+  return true;
+}
+int64_t extent(const View4& t, bool samples, bool rows) {
+  return t.d + (t.size[2] - 1) * t.stride[2] + (rows ? (t.size[1] - 1) * t.stride[1] : 0) +
+         (samples ? (t.size[0] - 1) * t.stride[0] : 0);
+}
+// Whether two views of the same samples and rows share no element: apart as a
+// whole, or side by side in each row or in each sample (views of one fused tensor).
+bool apart(const View4& s, const View4& t, size_t e) {
+  const View4 &a = s.at <= t.at ? s : t, &b = s.at <= t.at ? t : s;
+  const uintptr_t gap = b.at - a.at;
+  if (gap >= static_cast<uintptr_t>(extent(a, true, true)) * e) return true;
+  if (gap % e != 0 || a.size[0] != b.size[0] || a.size[1] != b.size[1]) return false;
+  const int64_t off = static_cast<int64_t>(gap / e);
+  for (int outer = 2; outer >= 1; --outer) {  // side by side in a row, in a sample
+    const bool rows = outer == 1;
+    bool same = true;
+    for (int i = 0; i < outer; ++i) same = same && (a.size[i] == 1 || a.stride[i] == b.stride[i]);
+    if (same && off >= extent(a, false, rows) && nested(off + extent(b, false, rows), a.size, a.stride, outer)) return true;
+  }
+  return false;
+}
+int mx_block(int fmt) { return fmt == SAFE_NVFP4 ? 16 : 32; }
+// Scale tiles along a row of D elements.
+int mx_tiles(int D, int fmt) { return (D / mx_block(fmt) + 3) / 4; }
+// The tensor's factor: 1 for the formats that have none; for nvfp4 within a
+// range that keeps 6 g, its inverse and every product with it normal numbers.
+bool mx_factor_ok(int fmt, float g) {
+  if (fmt < SAFE_MXFP8 || fmt > SAFE_NVFP4 || !std::isfinite(g)) return false;
+  return fmt == SAFE_NVFP4 ? g >= 0x1p-100f && g <= 0x1p100f : g == 1.f;
+}
+
+// Sets a kernel's shared-memory limit once for each device. (The kernel is a
+// template argument: instances of one kernel template share their type.)
+template <auto kKernel>
+bool allow_smem(int bytes) {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev >= 0 && dev < 64 && done[dev]) return true;
+  if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (dev >= 0 && dev < 64) done[dev] = true;
+  return true;
+}
+
+constexpr int kNormMaxVec = 512 * 8 * 10;  // longest row that rms_norm_kernel holds in registers
+
+template <typename T, int VEC, int NV, int TPR>
+void norm_launch(const NormParams& p, cudaStream_t s) {
+  constexpr int rows_cta = TPR < 128 ? 128 / TPR : 1;
+  rms_norm_kernel<T, VEC, NV, TPR>
+      <<<static_cast<unsigned>((p.rows_pad + rows_cta - 1) / rows_cta), TPR < 128 ? 128 : TPR, 0, s>>>(p);
+}
+
+// The fewest threads whose registers hold a row (a warp for each row needs no
+// barrier), then the smallest number of units for each.
+template <typename T>
+safe_status launch_norm(const NormParams& p, bool vec, cudaStream_t s) {
+  if (p.rows_pad > INT_MAX) return SAFE_ERR_UNSUPPORTED;
+  if (vec && p.D <= kNormMaxVec) {
+    const int units = p.D / 8;
+    if (units <= 32 * 2) norm_launch<T, 8, 2, 32>(p, s);
+    else if (units <= 32 * 4) norm_launch<T, 8, 4, 32>(p, s);
+    else if (units <= 32 * 6) norm_launch<T, 8, 6, 32>(p, s);
+    else if (units <= 32 * 8) norm_launch<T, 8, 8, 32>(p, s);
+    else if (units <= 32 * 10) norm_launch<T, 8, 10, 32>(p, s);
+    else if (units <= 128 * 4) norm_launch<T, 8, 4, 128>(p, s);
+    else if (units <= 128 * 7) norm_launch<T, 8, 7, 128>(p, s);
+    else if (units <= 128 * 10) norm_launch<T, 8, 10, 128>(p, s);
+    else if (units <= 512 * 5) norm_launch<T, 8, 5, 512>(p, s);
+    else norm_launch<T, 8, 10, 512>(p, s);
+  } else if (p.D <= 32 * 10) {
+    norm_launch<T, 1, 10, 32>(p, s);
+  } else if (p.D <= 128 * 10) {
+    norm_launch<T, 1, 10, 128>(p, s);
+  } else if (p.D <= 128 * 20) {
+    norm_launch<T, 1, 20, 128>(p, s);
+  } else {
+    rms_norm_long_kernel<T><<<static_cast<unsigned>(p.rows), 512, 0, s>>>(p);
+  }
+  return launch_status();
+}
+
+template <typename T>
+void launch_rope(const RopeParams& p, bool pairs, bool vec, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>((p.rows + kRopeWarps - 1) / kRopeWarps);
+  const size_t smem = static_cast<size_t>(kRopeWarps) * ((p.r / 2 + 3) & ~3) * sizeof(float2);
+  if (pairs) {
+    if (vec) rope_kernel<T, true, true><<<grid, 32 * kRopeWarps, smem, s>>>(p);
+    else rope_kernel<T, true, false><<<grid, 32 * kRopeWarps, smem, s>>>(p);
+  } else {
+    if (vec) rope_kernel<T, false, true><<<grid, 32 * kRopeWarps, smem, s>>>(p);
+    else rope_kernel<T, false, false><<<grid, 32 * kRopeWarps, smem, s>>>(p);
+  }
+}
+
+template <typename T>
+safe_status launch_mx_quantize(const MxQuantParams& p, int fmt, unsigned blocks, cudaStream_t s) {
+  if (fmt == SAFE_MXFP8) mx_quantize_kernel<T, kMxFp8><<<blocks, 256, 0, s>>>(p);
+  else if (fmt == SAFE_MXFP4) mx_quantize_kernel<T, kMxFp4><<<blocks, 256, 0, s>>>(p);
+  else mx_quantize_kernel<T, kNvFp4><<<blocks, 256, 0, s>>>(p);
+  return launch_status();
+}
+
+template <typename T>
+safe_status launch_mx_dequantize(const MxDecodeParams& p, int fmt, unsigned blocks, cudaStream_t s) {
+  if (fmt == SAFE_MXFP8) mx_dequantize_kernel<T, kMxFp8><<<blocks, 256, 0, s>>>(p);
+  else if (fmt == SAFE_MXFP4) mx_dequantize_kernel<T, kMxFp4><<<blocks, 256, 0, s>>>(p);
+  else mx_dequantize_kernel<T, kNvFp4><<<blocks, 256, 0, s>>>(p);
+  return launch_status();
+}
+
+// 2-D matrix [outer, inner] of bytes or 8-byte words (row pitch = inner); rows
+// and columns past it read as zero.
+bool encode_bytes_map(CUtensorMap* map, const void* base, bool words, uint64_t inner, uint64_t outer,
+                      uint32_t box_inner, uint32_t box_outer) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {inner * (words ? 8 : 1)};
+  cuuint32_t box[2] = {box_inner, box_outer};
+  cuuint32_t es[2] = {1, 1};
+  return fn(map, words ? CU_TENSOR_MAP_DATA_TYPE_UINT64 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base),
+            dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            words ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How many CTA pairs of a kernel can be resident at once on the current device.
+template <auto kKernel>
+int resident_pairs(int threads, int smem) {
+  static std::mutex mu;
+  static int cached[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const int sms = device_sms();
+  std::lock_guard<std::mutex> lock(mu);
+  int& n = cached[dev >= 0 && dev < 64 ? dev : 0];
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (sms / 2)));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    int c = 0;
+    n = cudaOccupancyMaxActiveClusters(&c, kKernel, &cfg) == cudaSuccess && c > 0 ? c : sms / 2;
+  }
+  return n;
+}
+
+template <int kFmt>
+safe_status launch_mx_linear(MxLinearParams& p, const void* X, const void* Xs, const void* W, const void* Ws, int d_in,
+                             cudaStream_t s) {
+  constexpr int smem = mx_linear_smem(kFmt), words = 64 * mx_stage_tiles(kFmt);
+  const uint64_t ct = static_cast<uint64_t>(mx_tiles(d_in, kFmt)) * 64, rb = static_cast<uint64_t>(p.row_bytes);
+  if (!encode_bytes_map(&p.x_map, X, false, rb, static_cast<uint64_t>(p.M), 128, 128) ||
+      !encode_bytes_map(&p.w_map, W, false, rb, static_cast<uint64_t>(p.d_out), 128, 96) ||
+      !encode_bytes_map(&p.xs_map, Xs, true, ct, static_cast<uint64_t>((p.M + 127LL) / 128), words, 1) ||
+      !encode_bytes_map(&p.ws_map, Ws, true, ct, static_cast<uint64_t>((p.d_out + 127) / 128), words, 2))
+    return SAFE_ERR_CUDA;
+  p.n_tiles = (p.d_out + kMxTileN - 1) / kMxTileN;
+  const int64_t tiles = (static_cast<int64_t>(p.M) + 255) / 256 * p.n_tiles;
+  if (tiles > INT_MAX) return SAFE_ERR_UNSUPPORTED;
+  p.tiles = static_cast<int>(tiles);
+  if (!allow_smem<mx_linear_pair_kernel<kFmt>>(smem)) return SAFE_ERR_CUDA;
+  const int mp = resident_pairs<mx_linear_pair_kernel<kFmt>>(kLinThreads, smem);
+  const int pairs = static_cast<int>(tiles < mp ? tiles : mp);
+  mx_linear_pair_kernel<kFmt><<<2 * pairs, kLinThreads, smem, s>>>(p);
+  return launch_status();
+}
+
 }  // namespace
 
 extern "C" {
@@ -808,6 +1015,236 @@ safe_status safe_gather_linear(const void* X, const int32_t* S, int k, const voi
     linear_kernel<<<grid, kLinThreads, kLinSmem, as_stream(stream)>>>(p);
   }
   return launch_status();
+}
+
+// ---------------------------------------------------------------- norm, positions, microscaled layers
+size_t safe_mx_scale_bytes(int64_t rows, int D, int fmt) {
+  if (rows < 1 || D < 1 || D % 32 != 0 || fmt < SAFE_MXFP8 || fmt > SAFE_NVFP4) return 0;
+  return static_cast<size_t>((rows + 127) / 128) * mx_tiles(D, fmt) * 512;
+}
+
+safe_status safe_rms_norm(const void* x, int x_full, const void* res, const int32_t* S, int k, const float* w,
+                          float eps, void* h, int h_full, void* y, void* q, void* q_scales, int dtype, int B, int N,
+                          int D, void* stream) {
+  const size_t e = float_size(dtype);
+  if (e == 0) return SAFE_ERR_UNSUPPORTED;
+  if (!sizes_ok(B, N, 1) || D < 1 || (S != nullptr && (k < 1 || k > N))) return SAFE_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || eps < 0.f) return SAFE_ERR_INVALID_ARG;
+  if (x == nullptr || (y == nullptr && q == nullptr) || (q == nullptr) != (q_scales == nullptr)) return SAFE_ERR_INVALID_ARG;
+  if (S == nullptr && (x_full || h_full)) return SAFE_ERR_INVALID_ARG;
+  if (h_full && (res == nullptr || h != res)) return SAFE_ERR_INVALID_ARG;  // the rows S of the stream, in place
+  if (!aligned_to(x, e) || !aligned_to(res, e) || !aligned_to(S, 4) || !aligned_to(w, 4) || !aligned_to(h, e) ||
+      !aligned_to(y, e))
+    return SAFE_ERR_INVALID_ARG;
+  if (!aligned_to(q, 16) || !aligned_to(q_scales, 16)) return SAFE_ERR_INVALID_ARG;
+  const int R = S != nullptr ? k : N;
+  NormParams p{};
+  p.rows = static_cast<long long>(B) * R;
+  const size_t n_full = static_cast<size_t>(B) * N * D, n_rows = static_cast<size_t>(p.rows) * D;
+  // outputs apart from each other and from the inputs; without S, h and y may
+  // take the place of x or res (each row is read before it is written)
+  const size_t xb = (x_full ? n_full : n_rows) * e, rb = n_full * e, ob = n_rows * e;
+  const size_t sb = q != nullptr ? safe_mx_scale_bytes(p.rows, D, SAFE_MXFP8) : 0;
+  auto clash = [&](const void* o, size_t obytes, const void* in, size_t ibytes) {
+    return overlap(o, obytes, in, ibytes) && !(S == nullptr && o == in);
+  };
+  if (clash(y, ob, x, xb) || clash(y, ob, res, rb) || clash(h, h_full ? 0 : ob, x, xb) ||
+      clash(h, h_full ? 0 : ob, res, rb) || overlap(h, h_full ? rb : ob, y, ob) || (h_full && overlap(h, rb, x, xb)))
+    return SAFE_ERR_INVALID_ARG;
+  if (q != nullptr) {
+    const void* in[] = {x, res, w, h, y};
+    const size_t len[] = {xb, rb, static_cast<size_t>(D) * 4, h_full ? rb : ob, ob};
+    for (int i = 0; i < 5; ++i)
+      if (overlap(q, n_rows, in[i], len[i]) || overlap(q_scales, sb, in[i], len[i])) return SAFE_ERR_INVALID_ARG;
+    if (overlap(q, n_rows, q_scales, sb)) return SAFE_ERR_INVALID_ARG;
+  }
+  const bool vec = D % 8 == 0 && aligned_to(x, 16) && aligned_to(res, 16) && aligned_to(w, 16) && aligned_to(h, 16) &&
+                   aligned_to(y, 16);
+  if (q != nullptr && (D % 32 != 0 || !vec)) return SAFE_ERR_INVALID_ARG;
+  if (q != nullptr && D > kNormMaxVec) return SAFE_ERR_UNSUPPORTED;
+  p.x = x;
+  p.res = res;
+  p.S = S;
+  p.w = w;
+  p.h = h;
+  p.y = y;
+  p.q = static_cast<uint8_t*>(q);
+  p.q_scales = static_cast<uint8_t*>(q_scales);
+  p.eps = eps;
+  p.N = N;
+  p.R = R;
+  p.D = D;
+  p.x_full = x_full ? 1 : 0;
+  p.h_full = h_full ? 1 : 0;
+  p.ct = q != nullptr ? mx_tiles(D, SAFE_MXFP8) : 0;
+  p.rows_pad = q != nullptr ? (p.rows + 127) / 128 * 128 : p.rows;
+  switch (dtype) {
+    case SAFE_F32: return launch_norm<float>(p, vec, as_stream(stream));
+    case SAFE_F16: return launch_norm<__half>(p, vec, as_stream(stream));
+    default: return launch_norm<__nv_bfloat16>(p, vec, as_stream(stream));
+  }
+}
+
+safe_status safe_rope(const void* q, const int64_t q_strides[3], void* oq, const int64_t oq_strides[3], int Hq,
+                      const void* k, const int64_t k_strides[3], void* ok, const int64_t ok_strides[3], int Hk,
+                      int dtype, const int64_t* freq, const int32_t* sections, int axes, const int32_t* pos,
+                      int pos_batched, const int32_t* S, int B, int N, int R, int d, int r, int interleaved, float m,
+                      void* stream) {
+  const size_t e = float_size(dtype);
+  if (e == 0) return SAFE_ERR_UNSUPPORTED;
+  if (q == nullptr || oq == nullptr || q_strides == nullptr || oq_strides == nullptr || Hq < 1) return SAFE_ERR_INVALID_ARG;
+  if (k == nullptr ? (ok != nullptr || Hk != 0) : (ok == nullptr || k_strides == nullptr || ok_strides == nullptr || Hk < 1))
+    return SAFE_ERR_INVALID_ARG;
+  if (!sizes_ok(B, N, Hq) || Hk > 65535 || R < 1 || R > N || (S == nullptr && R != N)) return SAFE_ERR_INVALID_ARG;
+  if (d < 2 || r < 2 || r > d || r % 2 != 0 || freq == nullptr || sections == nullptr || !std::isfinite(m))
+    return SAFE_ERR_INVALID_ARG;
+  if (axes < 1 || axes > 3 || (pos == nullptr && axes != 1)) return SAFE_ERR_INVALID_ARG;
+  if (d > 1024) return SAFE_ERR_UNSUPPORTED;
+  int sum = 0;
+  for (int a = 0; a < axes; ++a) {
+    if (sections[a] < 0 || sections[a] > r / 2) return SAFE_ERR_INVALID_ARG;
+    sum += sections[a];
+  }
+  if (sum != r / 2) return SAFE_ERR_INVALID_ARG;
+  if (!aligned_to(freq, 8) || !aligned_to(pos, 4) || !aligned_to(S, 4)) return SAFE_ERR_INVALID_ARG;
+  RopeParams p{};
+  bool vec = d % 8 == 0 && (interleaved ? r % 8 == 0 : r % 16 == 0);
+  const void* xs[2] = {q, k};
+  void* os[2] = {oq, ok};
+  const int64_t* st[4] = {q_strides, oq_strides, k_strides, ok_strides};
+  const int heads[2] = {Hq, Hk}, n = k != nullptr ? 2 : 1;
+  View4 in[2], out[2];
+  bool in_place[2] = {};
+  for (int i = 0; i < n; ++i) {
+    RopeTensor& t = p.t[i];
+    if (!aligned_to(xs[i], e) || !aligned_to(os[i], e)) return SAFE_ERR_INVALID_ARG;
+    for (int a = 0; a < 3; ++a) {
+      if (st[2 * i][a] < 0 || st[2 * i + 1][a] < 0) return SAFE_ERR_INVALID_ARG;
+      vec = vec && st[2 * i][a] % 8 == 0 && st[2 * i + 1][a] % 8 == 0;
+    }
+    const int64_t* o = st[2 * i + 1];
+    vec = vec && aligned_to(xs[i], 16) && aligned_to(os[i], 16);
+    t = RopeTensor{xs[i], os[i], st[2 * i][0], st[2 * i][1], st[2 * i][2], o[0], o[1], o[2], heads[i]};
+    in[i] = View4{reinterpret_cast<uintptr_t>(xs[i]), {B, R, heads[i]}, {t.xb, t.xn, t.xh}, d};
+    out[i] = View4{reinterpret_cast<uintptr_t>(os[i]), {B, R, heads[i]}, {t.ob, t.on, t.oh}, d};
+    if (!nested(d, out[i].size, out[i].stride, 3)) return SAFE_ERR_INVALID_ARG;
+    in_place[i] = xs[i] == os[i] && t.xb == t.ob && t.xn == t.on && t.xh == t.oh;
+    if (!in_place[i]) p.copy_tail = r < d;
+  }
+  // an output shares no element with the other one, nor with an input that is not its own in place
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < n; ++j)
+      if ((i != j || !in_place[i]) && !apart(out[i], in[j], e)) return SAFE_ERR_INVALID_ARG;
+  if (n == 2 && !apart(out[0], out[1], e)) return SAFE_ERR_INVALID_ARG;
+  p.freq = reinterpret_cast<const long long*>(freq);
+  p.pos = pos;
+  p.pos_b = pos_batched ? static_cast<long long>(N) * axes : 0;
+  p.S = S;
+  p.axes = axes;
+  p.sec0 = sections[0];
+  p.sec1 = axes > 1 ? sections[1] : 0;
+  p.N = N;
+  p.R = R;
+  p.d = d;
+  p.r = r;
+  p.m = m;
+  p.rows = static_cast<long long>(B) * R;  // <= B N <= INT_MAX
+  cudaStream_t s = as_stream(stream);
+  switch (dtype) {
+    case SAFE_F32: launch_rope<float>(p, interleaved != 0, vec, s); break;
+    case SAFE_F16: launch_rope<__half>(p, interleaved != 0, vec, s); break;
+    default: launch_rope<__nv_bfloat16>(p, interleaved != 0, vec, s);
+  }
+  return launch_status();
+}
+
+safe_status safe_mx_quantize(const void* X, int dtype, const int32_t* S, int k, int fmt, float g, void* data,
+                             void* scales, int B, int N, int D, void* stream) {
+  if (float_size(dtype) == 0) return SAFE_ERR_UNSUPPORTED;
+  if (!aligned16(X) || !aligned16(data) || !aligned16(scales) || !aligned_to(S, 4)) return SAFE_ERR_INVALID_ARG;
+  if (!sizes_ok(B, N, 1) || (S != nullptr && (k < 1 || k > N)) || D < 32 || D % 32 != 0) return SAFE_ERR_INVALID_ARG;
+  if (!mx_factor_ok(fmt, g)) return SAFE_ERR_INVALID_ARG;
+  MxQuantParams p{};
+  p.X = X;
+  p.S = S;
+  p.data = static_cast<uint8_t*>(data);
+  p.scales = static_cast<uint8_t*>(scales);
+  p.g = g;
+  p.inv6g = 1.f / (6.f * g);
+  p.B = B;
+  p.N = N;
+  p.R = S != nullptr ? k : N;
+  p.D = D;
+  p.ct = mx_tiles(D, fmt);
+  p.upr = p.ct * 4 * (fmt == SAFE_NVFP4 ? 1 : 2);
+  p.rows = static_cast<long long>(B) * p.R;
+  p.rows_pad = (p.rows + 127) / 128 * 128;
+  const size_t db = static_cast<size_t>(p.rows) * (fmt == SAFE_MXFP8 ? D : D / 2);
+  const size_t sb = safe_mx_scale_bytes(p.rows, D, fmt), xb = static_cast<size_t>(B) * N * D * float_size(dtype);
+  if (overlap(data, db, X, xb) || overlap(scales, sb, X, xb) || overlap(data, db, scales, sb)) return SAFE_ERR_INVALID_ARG;
+  const long long blocks = (p.rows_pad * p.upr + 256 * kMxUnroll - 1) / (256 * kMxUnroll);
+  if (blocks > INT_MAX) return SAFE_ERR_UNSUPPORTED;
+  switch (dtype) {
+    case SAFE_F32: return launch_mx_quantize<float>(p, fmt, static_cast<unsigned>(blocks), as_stream(stream));
+    case SAFE_F16: return launch_mx_quantize<__half>(p, fmt, static_cast<unsigned>(blocks), as_stream(stream));
+    default: return launch_mx_quantize<__nv_bfloat16>(p, fmt, static_cast<unsigned>(blocks), as_stream(stream));
+  }
+}
+
+safe_status safe_mx_dequantize(const void* data, const void* scales, int fmt, float g, void* Y, int dtype,
+                               int64_t rows, int D, void* stream) {
+  if (float_size(dtype) == 0) return SAFE_ERR_UNSUPPORTED;
+  if (!aligned16(data) || !aligned16(scales) || !aligned16(Y)) return SAFE_ERR_INVALID_ARG;
+  if (rows < 1 || rows > INT_MAX || D < 32 || D % 32 != 0 || !mx_factor_ok(fmt, g)) return SAFE_ERR_INVALID_ARG;
+  const size_t db = static_cast<size_t>(rows) * (fmt == SAFE_MXFP8 ? D : D / 2);
+  const size_t yb = static_cast<size_t>(rows) * D * float_size(dtype);
+  if (overlap(Y, yb, data, db) || overlap(Y, yb, scales, safe_mx_scale_bytes(rows, D, fmt))) return SAFE_ERR_INVALID_ARG;
+  MxDecodeParams p{};
+  p.data = static_cast<const uint8_t*>(data);
+  p.scales = static_cast<const uint8_t*>(scales);
+  p.Y = Y;
+  p.g = g;
+  p.D = D;
+  p.ct = mx_tiles(D, fmt);
+  p.upr = D / 16;
+  p.units = static_cast<long long>(rows) * p.upr;
+  const long long blocks = (p.units + 255) / 256;
+  if (blocks > INT_MAX) return SAFE_ERR_UNSUPPORTED;
+  switch (dtype) {
+    case SAFE_F32: return launch_mx_dequantize<float>(p, fmt, static_cast<unsigned>(blocks), as_stream(stream));
+    case SAFE_F16: return launch_mx_dequantize<__half>(p, fmt, static_cast<unsigned>(blocks), as_stream(stream));
+    default: return launch_mx_dequantize<__nv_bfloat16>(p, fmt, static_cast<unsigned>(blocks), as_stream(stream));
+  }
+}
+
+safe_status safe_mx_linear(const void* X, const void* X_scales, const void* Wt, const void* Wt_scales, int fmt,
+                           float alpha, const float* bias, int act, void* Y, int64_t rows, int d_in, int d_out,
+                           void* stream) {
+  if (!aligned16(X) || !aligned16(X_scales) || !aligned16(Wt) || !aligned16(Wt_scales) || !aligned16(Y) ||
+      !aligned_to(bias, 4))
+    return SAFE_ERR_INVALID_ARG;
+  if (fmt < SAFE_MXFP8 || fmt > SAFE_NVFP4 || !std::isnormal(alpha) || (act != 0 && act != 1)) return SAFE_ERR_INVALID_ARG;
+  if (rows < 1 || rows > INT_MAX || d_in < 64 || d_in % 32 != 0 || d_out < 8 || d_out % 8 != 0) return SAFE_ERR_INVALID_ARG;
+  const int row_bytes = fmt == SAFE_MXFP8 ? d_in : d_in / 2;
+  const size_t yb = static_cast<size_t>(rows) * d_out * 2;
+  if (overlap(Y, yb, X, static_cast<size_t>(rows) * row_bytes) ||
+      overlap(Y, yb, X_scales, safe_mx_scale_bytes(rows, d_in, fmt)) ||
+      overlap(Y, yb, Wt, static_cast<size_t>(d_out) * row_bytes) ||
+      overlap(Y, yb, Wt_scales, safe_mx_scale_bytes(d_out, d_in, fmt)))
+    return SAFE_ERR_INVALID_ARG;
+  MxLinearParams p{};
+  p.bias = bias;
+  p.Y = static_cast<__nv_bfloat16*>(Y);
+  p.alpha = alpha;
+  p.M = static_cast<int>(rows);
+  p.row_bytes = row_bytes;
+  p.d_out = d_out;
+  p.act = act;
+  switch (fmt) {
+    case SAFE_MXFP8: return launch_mx_linear<kMxFp8>(p, X, X_scales, Wt, Wt_scales, d_in, as_stream(stream));
+    case SAFE_MXFP4: return launch_mx_linear<kMxFp4>(p, X, X_scales, Wt, Wt_scales, d_in, as_stream(stream));
+    default: return launch_mx_linear<kNvFp4>(p, X, X_scales, Wt, Wt_scales, d_in, as_stream(stream));
+  }
 }
 
 safe_status safe_partition_indicator(const int32_t* S, int k, float* s, int B, int N, void* stream) {

@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-from typing import Optional, Tuple
+from typing import Optional, Sequence, Tuple
 
 import torch
 
@@ -23,6 +23,7 @@ SAFE_OK, SAFE_ERR_INVALID_ARG, SAFE_ERR_UNSUPPORTED, SAFE_ERR_CUDA, SAFE_ERR_TIM
 _MASK_DTYPES = {torch.bool: 0, torch.uint8: 1, torch.float32: 2, torch.float16: 3, torch.bfloat16: 4}
 
 _vp, _i, _f, _i64p, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.POINTER(ctypes.c_int64), ctypes.c_size_t
+_i64, _i32p = ctypes.c_int64, ctypes.POINTER(ctypes.c_int32)
 
 # name -> argtypes (restype is int for every entry point except the ones listed)
 _SIGS = {
@@ -52,10 +53,17 @@ _SIGS = {
     "safe_sw_cfg": [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _f, _vp],
     "safe_gather_linear_workspace_bytes": [_i, _i, _i],
     "safe_gather_linear": [_vp, _vp, _i, _vp, _vp, _i, _vp, _i, _i, _i, _i, _vp, _sz, _vp],
+    "safe_rms_norm": [_vp, _i, _vp, _vp, _i, _vp, _f, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _vp],
+    "safe_rope": [_vp, _i64p, _vp, _i64p, _i, _vp, _i64p, _vp, _i64p, _i, _i, _vp, _i32p, _i, _vp, _i, _vp, _i, _i, _i,
+                  _i, _i, _i, _f, _vp],
+    "safe_mx_scale_bytes": [_i64, _i, _i],
+    "safe_mx_quantize": [_vp, _i, _vp, _i, _i, _f, _vp, _vp, _i, _i, _i, _vp],
+    "safe_mx_dequantize": [_vp, _vp, _i, _f, _vp, _i, _i64, _i, _vp],
+    "safe_mx_linear": [_vp, _vp, _vp, _vp, _i, _f, _vp, _i, _vp, _i64, _i, _i, _vp],
 }
 _RESTYPES = {"safe_pcsp_workspace_bytes": _sz, "safe_attn_workspace_bytes": _sz, "safe_sensitivity_workspace_bytes": _sz,
              "safe_gather_linear_workspace_bytes": _sz, "safe_srsu_workspace_bytes": _sz,
-             "safe_status_string": ctypes.c_char_p}
+             "safe_mx_scale_bytes": _sz, "safe_status_string": ctypes.c_char_p}
 
 
 class SafeError(RuntimeError):
@@ -504,4 +512,399 @@ def gather_linear(X, Wt, S=None, bias=None, act="none", out=None, ws=None):
         w, wb = ws, ws.numel()
     _check("safe_gather_linear", lib().safe_gather_linear(_p(X), _p(S), k, _p(Wt), _p(bias), _ACTS[act], _p(out), B,
                                                           N, d_in, d_out, _p(w), wb, _stream()))
+    return out
+
+
+# ---------------------------------------------------------------- norm, positions, microscaled layers
+_FLOATS = {torch.float32: 2, torch.float16: 3, torch.bfloat16: 4}
+_FORMATS = {"mxfp8": 0, "mxfp4": 1, "nvfp4": 2}
+_i64x3 = ctypes.c_int64 * 3
+
+
+def _run(name: str, dev: torch.device, *args):
+    """Call entry point `name` on `dev` (which need not be the current device)
+    with that device's current stream as the last argument."""
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            st = getattr(lib(), name)(*args, _stream())
+    else:
+        st = getattr(lib(), name)(*args, _stream())
+    if st != SAFE_OK:
+        raise SafeError(name, st)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _float_code(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.dtype not in _FLOATS:
+        raise ValueError(f"{name} must be a float32, float16 or bfloat16 tensor")
+    return _FLOATS[t.dtype]
+
+
+def _rows_of(S, B: int, N: int, dev) -> int:
+    """Rows of each sample: N, or k of S [B, k] (checked)."""
+    if S is None:
+        return N
+    _need(S, "S", torch.int32, 2, device=dev)
+    k = S.shape[1]
+    if S.shape[0] != B or not 1 <= k <= N:
+        raise ValueError(f"S must have shape ({B}, 1..{N}), got {tuple(S.shape)}")
+    return k
+
+
+class MxTensor:
+    """A microscaled matrix: `data` [..., D] e4m3 (mxfp8) or [..., D / 2] uint8
+    (mxfp4, nvfp4: two e2m1 to a byte, the even element in the low half),
+    `scales` the scale bytes in tiles of 128 rows x 4 (flat uint8, the rows of
+    data's leading dims one after another; layout: safe_mx_quantize in
+    include/safe_attn.h), `fmt` "mxfp8", "mxfp4" or "nvfp4", and `scale` the
+    factor of the whole matrix (nvfp4; 1 otherwise)."""
+
+    __slots__ = ("data", "scales", "fmt", "scale")
+
+    def __init__(self, data: torch.Tensor, scales: torch.Tensor, fmt: str, scale: float = 1.0):
+        if fmt not in _FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(_FORMATS)}, got {fmt!r}")
+        want = torch.float8_e4m3fn if fmt == "mxfp8" else torch.uint8
+        if not isinstance(data, torch.Tensor) or data.dim() < 2:
+            raise ValueError("data must be a tensor of at least 2 dims")
+        _need(data, "data", want, data.dim())
+        rows, D = _mx_rows(data, fmt)
+        _need(scales, "scales", torch.uint8, 1, (mx_scale_bytes(rows, D, fmt),), data.device)
+        self.data, self.scales, self.fmt, self.scale = data, scales, fmt, _factor(fmt, scale)
+
+    @property
+    def shape(self) -> Tuple[int, ...]:
+        """The shape of the values that the matrix stands for."""
+        return (*self.data.shape[:-1], _mx_rows(self.data, self.fmt)[1])
+
+    @property
+    def device(self) -> torch.device:
+        return self.data.device
+
+
+def _mx_rows(data: torch.Tensor, fmt: str):
+    """(rows, D) of a microscaled matrix's elements."""
+    w = data.shape[-1]
+    D = w if fmt == "mxfp8" else 2 * w
+    if D < 32 or D % 32 or data.numel() == 0:
+        raise ValueError(f"rows of a microscaled matrix have a multiple of 32 elements, got {tuple(data.shape)}")
+    return data.numel() // w, D
+
+
+def mx_scale_bytes(rows: int, D: int, fmt: str) -> int:
+    """Bytes of the scales of a microscaled [rows, D] matrix (0: no such form)."""
+    if fmt not in _FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(_FORMATS)}, got {fmt!r}")
+    if rows < 1 or D < 1 or D % 32:
+        return 0
+    return -(-rows // 128) * -(-D // (64 if fmt == "nvfp4" else 128)) * 512
+
+
+def _mx_new(lead, D: int, fmt: str, scale: float, dev) -> MxTensor:
+    """A microscaled matrix [*lead, D] of undefined contents."""
+    m = MxTensor.__new__(MxTensor)  # made to fit: nothing to check
+    rows = math.prod(lead)
+    if fmt == "mxfp8":
+        m.data = torch.empty((*lead, D), dtype=torch.float8_e4m3fn, device=dev)
+    else:
+        m.data = torch.empty((*lead, D // 2), dtype=torch.uint8, device=dev)
+    m.scales = torch.empty(mx_scale_bytes(rows, D, fmt), dtype=torch.uint8, device=dev)
+    m.fmt, m.scale = fmt, float(scale)
+    return m
+
+
+def _mx_out(out, lead, D: int, fmt: str, scale: float, dev) -> MxTensor:
+    if out is None:
+        return _mx_new(lead, D, fmt, scale, dev)
+    if not isinstance(out, MxTensor) or out.fmt != fmt or out.shape != (*lead, D) or out.device != dev:
+        raise ValueError(f"out must be an MxTensor {fmt} of shape {(*lead, D)} on {dev}")
+    out.scale = float(scale)
+    return out
+
+
+def rms_norm(x, w=None, residual=None, S=None, eps=1e-6, x_compact=False, quant=None, update=False, out=None, h=None):
+    """Root-mean-square norm of rows with the residual's addition: h = x +
+    residual, y = h / sqrt(mean(h^2) + eps) * w; returns y, or (y, h) with a
+    residual. x [B, N, D] (fp32, fp16 or bf16), residual [B, N, D] of the same
+    type, w [D] fp32 or None.
+    S [B, k] int32: only the rows S of the stream (Eq. (13)); x then is
+    [B, k, D] with x_compact (a row-selective branch's output), else [B, N, D],
+    and y, h are [B, k, D].
+    quant "mxfp8": y is an MxTensor (8 bits with a scale for each 32
+    elements), as mx_linear takes it; D is then a multiple of 32.
+    update: h is the residual itself, its rows (of S, strictly ascending, or
+    all) updated in place. out, h: buffers for the results."""
+    dt = _float_code(x, "x")
+    _need(x, "x", x.dtype, 3)
+    dev = x.device
+    src = x if residual is None else residual
+    if residual is not None:
+        _need(residual, "residual", x.dtype, 3, device=dev)
+    B, N, D = src.shape
+    k = 0
+    if residual is None and S is not None and x_compact:
+        raise ValueError("x_compact needs a residual: the rows of S are already gathered in x")
+    R = _rows_of(S, B, N, dev)
+    if S is not None:
+        k = R
+    full = S is not None and not x_compact
+    _need(x, "x", x.dtype, 3, (B, N if full else R, D), dev)
+    if w is not None:
+        _need(w, "w", torch.float32, 1, (D,), dev)
+    if quant not in (None, "mxfp8"):
+        raise ValueError(f"quant must be None or 'mxfp8', got {quant!r}")
+    if (update or h is not None) and residual is None:
+        raise ValueError("update and h need a residual")
+    if update and h is not None:
+        raise ValueError("update writes the sums to the residual: h must be None")
+    if residual is not None:
+        h = residual if update else _out(h, "h", x.dtype, (B, R, D), dev)
+    if quant is None:
+        y = _out(out, "out", x.dtype, (B, R, D), dev)
+        yp, qp, sp = y.data_ptr(), None, None
+    else:
+        if D % 32:
+            raise ValueError(f"an 8-bit output needs D a multiple of 32, got {D}")
+        y = _mx_out(out, (B, R), D, quant, 1.0, dev)
+        yp, qp, sp = None, y.data.data_ptr(), y.scales.data_ptr()
+    _run("safe_rms_norm", dev, x.data_ptr(), 1 if full else 0, _ptr(residual), _ptr(S), k, _ptr(w), eps, _ptr(h),
+         1 if update and S is not None else 0, yp, qp, sp, dt, B, N, D)
+    return y if residual is None else (y, h)
+
+
+class RopeTable:
+    """The frequencies of rotary positions (made by rope_table): `freq` [r / 2]
+    int64 in 2^-64 turns, `sections` the pairs of each position axis, `m` the
+    factor on the rotated elements."""
+
+    __slots__ = ("freq", "sections", "m", "r", "_sections")
+
+    def __init__(self, freq: torch.Tensor, sections: Sequence[int], m: float = 1.0):
+        _need(freq, "freq", torch.int64, 1)
+        self.sections = tuple(int(n) for n in sections)
+        self.r = 2 * freq.shape[0]
+        if not 1 <= len(self.sections) <= 3 or min(self.sections) < 0 or 2 * sum(self.sections) != self.r or self.r < 2:
+            raise ValueError(f"sections must be 1 to 3 counts that share out {self.r // 2} pairs, got {self.sections}")
+        if not math.isfinite(m):
+            raise ValueError(f"m must be finite, got {m}")
+        self.freq, self.m = freq, float(m)
+        self._sections = (ctypes.c_int32 * len(self.sections))(*self.sections)
+
+
+def rope_frequencies(r: int, base: float = 10000.0, sections: Optional[Sequence[int]] = None, kind: str = "none",
+                     factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                     attn_factor: Optional[float] = None):
+    """(frequencies in radians for each position of the r / 2 pairs, factor m on
+    the rotated elements). An axis with n pairs has r' = 2 n and the
+    frequencies base^(-2 i / r'), stretched for contexts `factor` times longer:
+      linear  divided by factor
+      ntk     base * factor^(r' / (r' - 2)): the last is divided by factor, the first kept
+      yarn    pairs that turn more than beta_fast times over original_len are
+              kept, those below beta_slow turns divided by factor, a ramp over
+              the pairs in between; m = 0.1 ln(factor) + 1 (or attn_factor)."""
+    if r < 2 or r % 2:
+        raise ValueError(f"r must be even and at least 2, got {r}")
+    sections = [r // 2] if sections is None else [int(n) for n in sections]
+    if not 1 <= len(sections) <= 3 or min(sections) < 0 or 2 * sum(sections) != r:
+        raise ValueError(f"sections must be 1 to 3 counts that share out {r // 2} pairs, got {sections}")
+    if kind not in ("none", "linear", "ntk", "yarn"):
+        raise ValueError(f"kind must be none, linear, ntk or yarn, got {kind!r}")
+    if not base > 1 or not math.isfinite(base) or not factor >= 1 or not math.isfinite(factor):
+        raise ValueError(f"base must be above 1 and factor at least 1, got {base} and {factor}")
+    if kind == "yarn" and (original_len < 1 or not 0 < beta_slow < beta_fast):
+        raise ValueError("yarn needs original_len and 0 < beta_slow < beta_fast")
+    f = []
+    for n in sections:
+        b = base * factor ** (n / (n - 1)) if kind == "ntk" and n > 1 else base
+        w = [b ** (-i / n) for i in range(n)]
+        if kind == "linear":
+            w = [v / factor for v in w]
+        elif kind == "yarn" and n:
+            # the pair that turns `t` times over the original length
+            lo, hi = (n * math.log(original_len / (2 * math.pi * t)) / math.log(base) for t in (beta_fast, beta_slow))
+            lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), 2 * n - 1)
+            ramp = [min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(n)]
+            w = [v / factor * t + v * (1 - t) for v, t in zip(w, ramp)]
+        f += w
+    m = 1.0
+    if kind == "yarn":
+        m = 0.1 * math.log(factor) + 1.0
+    return f, m if attn_factor is None else float(attn_factor)
+
+
+def rope_table(r: int, base: float = 10000.0, sections: Optional[Sequence[int]] = None, device="cuda", **scaling):
+    """The table of rotary positions that rope takes; arguments:
+    rope_frequencies. sections share the r / 2 pairs out over up to three
+    position axes (e.g. rows and columns of the latent grid)."""
+    f, m = rope_frequencies(r, base, sections, **scaling)
+    turns = [int(math.ldexp(v / (2 * math.pi), 64)) & (2 ** 64 - 1) for v in f]
+    freq = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+    return RopeTable(freq, [r // 2] if sections is None else sections, m)
+
+
+def _heads(t, name: str, dtype, B, R, d, dev):
+    """Check a [B, R, H, d] tensor or view (contiguous in d); returns H, strides."""
+    if not isinstance(t, torch.Tensor) or not _on_device(t) or t.device != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+    shape = t.shape
+    if t.dtype != dtype or len(shape) != 4 or shape[0] != B or shape[1] != R or shape[2] < 1 or shape[3] != d:
+        raise ValueError(f"{name} must be {dtype} of shape ({B}, {R}, heads, {d}), got {t.dtype} {tuple(shape)}")
+    st = t.stride()
+    if st[3] != 1:
+        raise ValueError(f"{name} must be contiguous in its last dim")
+    return shape[2], _i64x3(st[0], st[1], st[2])
+
+
+def rope(q, k, table: RopeTable, pos=None, S=None, interleaved=False, inplace=False, out=None):
+    """Rotary positions: every pair of the first table.r elements of a head
+    turns by position * frequency. q [B, R, H, d], k [B, R, Hk, d] or None
+    (fp32, fp16 or bf16; views of a fused projection too, contiguous in the
+    last dim). pos: int32 [N, axes] shared by the samples (one axis: [N] will
+    do) or [B, N, axes]; None: the token index. S [B, R] int32: row r is token
+    S[b, r], else token r. interleaved: pairs
+    (2i, 2i + 1) instead of (i, i + r / 2). Returns (q, k) turned: new
+    contiguous tensors, those of out=(q, k), or with inplace q and k
+    themselves."""
+    dt = _float_code(q, "q")
+    if not isinstance(table, RopeTable):
+        raise ValueError("table must be a RopeTable")
+    if q.dim() != 4:
+        raise ValueError(f"q must have 4 dims, got {tuple(q.shape)}")
+    B, R, _, d = q.shape
+    dev, axes = q.device, len(table.sections)
+    H, qs = _heads(q, "q", q.dtype, B, R, d, dev)
+    Hk, ks, oks = 0, None, None
+    if k is not None:
+        Hk, ks = _heads(k, "k", q.dtype, B, R, d, dev)
+    if table.freq.device != dev:
+        raise ValueError(f"table must be on {dev}")
+    if table.r > d:
+        raise ValueError(f"the table turns {table.r} elements, heads have {d}")
+    N, batched = R, 0
+    if pos is None:
+        if axes != 1:
+            raise ValueError(f"a table of {axes} axes needs pos")
+        if S is not None:
+            raise ValueError("S needs pos (the positions of all tokens)")
+    else:
+        nd = pos.dim()
+        if nd == 1 and axes == 1:
+            N, want = pos.shape[0], None
+        elif nd in (2, 3):
+            batched, N = nd - 2, pos.shape[-2]
+            want = (B, N, axes) if batched else (N, axes)
+        else:
+            raise ValueError(f"pos must be [tokens, {axes}] or [{B}, tokens, {axes}], got {tuple(pos.shape)}")
+        _need(pos, "pos", torch.int32, nd, want, dev)
+    if S is not None:
+        _need(S, "S", torch.int32, 2, (B, R), dev)
+        if R > N:
+            raise ValueError(f"S names {R} rows of {N} tokens")
+    elif N != R:
+        raise ValueError(f"pos has {N} tokens, q {R} rows")
+    if inplace:
+        if out is not None:
+            raise ValueError("inplace writes to q and k: out must be None")
+        oq, ok, oqs, oks = q, k, qs, ks
+    else:
+        oq, ok = (None, None) if out is None else out
+        if oq is None:
+            oq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            oqs = _i64x3(R * H * d, H * d, d)
+        else:
+            n, oqs = _heads(oq, "out[0]", q.dtype, B, R, d, dev)
+            if n != H:
+                raise ValueError(f"out[0] must have {H} heads, got {n}")
+        if k is None:
+            if ok is not None:
+                raise ValueError("out[1] needs k")
+        elif ok is None:
+            ok = torch.empty(k.shape, dtype=q.dtype, device=dev)
+            oks = _i64x3(R * Hk * d, Hk * d, d)
+        else:
+            n, oks = _heads(ok, "out[1]", q.dtype, B, R, d, dev)
+            if n != Hk:
+                raise ValueError(f"out[1] must have {Hk} heads, got {n}")
+    _run("safe_rope", dev, q.data_ptr(), qs, oq.data_ptr(), oqs, H, _ptr(k), ks, _ptr(ok), oks, Hk, dt,
+         table.freq.data_ptr(), table._sections, axes, _ptr(pos), batched, _ptr(S), B, N, R, d, table.r,
+         1 if interleaved else 0, table.m)
+    return oq, ok
+
+
+def _factor(fmt: str, scale: float) -> float:
+    """The factor of a microscaled matrix as the fp32 number that is kept."""
+    s = ctypes.c_float(scale).value
+    if fmt == "nvfp4" and not 2.0 ** -100 <= s <= 2.0 ** 100:
+        raise ValueError(f"scale must lie in [2^-100, 2^100], got {scale}")
+    if fmt != "nvfp4" and s != 1.0:
+        raise ValueError(f"{fmt} has no factor of the whole matrix: scale must be 1, got {scale}")
+    return s
+
+
+def mx_quantize(x, fmt: str, S=None, scale: float = 1.0, out=None) -> MxTensor:
+    """The rows of x [B, N, D] (or [N, D]: a weight; fp32, fp16 or bf16), or its
+    rows S [B, k], in microscaled 8 or 4 bits: fmt "mxfp8", "mxfp4" or "nvfp4".
+    scale: the factor of an nvfp4 matrix (largest magnitude / 2688 lets every
+    block scale be represented). Returns an MxTensor [B, k or N, D]."""
+    dt = _float_code(x, "x")
+    if fmt not in _FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(_FORMATS)}, got {fmt!r}")
+    nd = x.dim()
+    if nd not in (2, 3):
+        raise ValueError(f"x must have 2 or 3 dims, got {tuple(x.shape)}")
+    _need(x, "x", x.dtype, nd)
+    B, N, D = x.shape if nd == 3 else (1, *x.shape)
+    if D < 32 or D % 32:
+        raise ValueError(f"rows must have a multiple of 32 elements, got {D}")
+    dev, g = x.device, _factor(fmt, scale)
+    if S is not None and nd == 2:
+        raise ValueError("S needs x of 3 dims")
+    R = _rows_of(S, B, N, dev)
+    m = _mx_out(out, (B, R) if nd == 3 else (N,), D, fmt, g, dev)
+    _run("safe_mx_quantize", dev, x.data_ptr(), dt, _ptr(S), R if S is not None else 0, _FORMATS[fmt], g,
+         m.data.data_ptr(), m.scales.data_ptr(), B, N, D)
+    return m
+
+
+def mx_dequantize(m: MxTensor, dtype=torch.bfloat16, out=None):
+    """The values that a microscaled matrix stands for, rounded to dtype."""
+    if not isinstance(m, MxTensor):
+        raise ValueError("m must be an MxTensor")
+    if dtype not in _FLOATS:
+        raise ValueError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    rows, D = _mx_rows(m.data, m.fmt)
+    dev = m.device
+    out = _out(out, "out", dtype, (*m.data.shape[:-1], D), dev)
+    _run("safe_mx_dequantize", dev, m.data.data_ptr(), m.scales.data_ptr(), _FORMATS[m.fmt], m.scale, out.data_ptr(),
+         _FLOATS[dtype], rows, D)
+    return out
+
+
+def mx_linear(X: MxTensor, W: MxTensor, bias=None, act="none", out=None):
+    """A row-wise layer with microscaled operands, Y = act(X W^T + bias): X
+    [..., d_in] (mx_quantize, rms_norm with quant; the rows of S for the
+    row-selective block), W [d_out, d_in], both of one format; bias [d_out]
+    fp32, act "none" or "gelu_tanh". Returns bf16 [..., d_out]."""
+    if not isinstance(X, MxTensor) or not isinstance(W, MxTensor):
+        raise ValueError("X and W must be MxTensors")
+    if X.fmt != W.fmt:
+        raise ValueError(f"X is {X.fmt}, W is {W.fmt}: both operands must have one format")
+    rows, d_in = _mx_rows(X.data, X.fmt)
+    d_out, dw = W.data.shape[0], _mx_rows(W.data, W.fmt)[1]
+    dev = X.device
+    if W.data.dim() != 2 or dw != d_in or W.device != dev:
+        raise ValueError(f"W must be [d_out, {d_in}] on {dev}, got {W.shape} on {W.device}")
+    if bias is not None:
+        _need(bias, "bias", torch.float32, 1, (d_out,), dev)
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    alpha = X.scale * W.scale
+    if not 2.0 ** -126 <= abs(alpha) < 2.0 ** 128:
+        raise ValueError(f"the product of the operands' factors is out of range: {alpha}")
+    out = _out(out, "out", torch.bfloat16, (*X.data.shape[:-1], d_out), dev)
+    _run("safe_mx_linear", dev, X.data.data_ptr(), X.scales.data_ptr(), W.data.data_ptr(), W.scales.data_ptr(),
+         _FORMATS[X.fmt], alpha, _ptr(bias), _ACTS[act], out.data_ptr(), rows, d_in, d_out)
     return out
