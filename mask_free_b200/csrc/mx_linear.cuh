@@ -6,21 +6,32 @@
 // to each block's products and adds in fp32 (tcgen05.mma .block_scale).
 //
 // linear_pair_kernel's structure with other operands: a CTA pair computes
-// 256 x 192 output tiles, each CTA 128 rows. A stage of the ring is 128
+// 256 x 256 output tiles, each CTA 128 rows. A stage of the ring is 128
 // bytes of every row (128 e4m3 or 256 e2m1 elements, four MMA steps of 32
 // bytes) with the scales that belong to them:
-//   A       the CTA's 128 rows x 128 B            16 KB
-//   B       the CTA's 96 of the 192 W rows        12 KB
-//   scale A of the CTA's own rows (one scale tile for each 4 scales of a row)
-//   scale B of all 192 W rows, in both CTAs: two scale tiles high, since a
-//           tile of columns begins in the middle of one when its index is odd
+//   A, B     128 rows x 128 B each: the CTA's rows of X and its half of the W rows
+//   scale A  of the CTA's own rows (one scale tile for each 4 scales of a row)
+//   scale B  of all 256 W rows, in both CTAs
 // Scales travel shared memory -> TMEM by tcgen05.cp (32 lanes x 16 B, copied
 // to all four lane quarters) right before the MMAs that use them; copies and
-// MMAs of one thread run in order, and two scale buffers let the next
-// stage's copies pass the current MMAs. TMEM: two 192-column accumulators
-// (tile i uses i & 1) and the two scale buffers of 48 columns: 480 of 512.
-// With 256 columns the second accumulator would not fit beside the scales,
-// and every tile's MMAs would wait for the last tile's epilogue.
+// MMAs of one thread run in order, so one scale buffer serves every stage.
+// TMEM (512 columns): the last 64 hold the scales; the two accumulators of
+// 256 columns (tile i uses i & 1) overlap in 64 columns in the middle, the last
+// of accumulator 0 and the first of 1. In the last stage of a tile the MMAs
+// of these shared columns come first, in the first stage of the next they
+// come last, so that the epilogue reads them while the other 192 columns are
+// multiplied, and the tensor core does not wait for it. (For these two stages
+// each CTA holds 96 + 32 rows of W, its halves of the two parts, instead of
+// 128: the columns' order stays that of the rows of W.)
+//
+// What bounds it: a stage is 38 KB into shared memory and 38 KB out of it for
+// 512 cycles of MMA, and 1000 W: at K = 9216 nvfp4 runs at 6.1 PFLOP/s with
+// the clock down to 1.45 GHz (mxfp8 2.9 at 1.25 GHz). Measured before: tiles
+// of 192 columns with accumulators apart, 4.2 / 4.9 PFLOP/s (K = 2304 / 9216,
+// nvfp4, 51200 and 12800 x 6912) against 4.8 / 6.1 of these; accumulators that
+// overlap without the split, 4.6 / 5.6 (the tensor core idles 1100 cycles
+// at each tile); the output through shared memory and tiled stores, 4.4 - 4.6
+// at K = 2304 (its 128 KB compete with the operands) against 4.8.
 #pragma once
 
 #include "linear.cuh"
@@ -73,6 +84,42 @@ __device__ __forceinline__ void umma_pair_mx_if(uint32_t leader, uint32_t d_tmem
   }
 }
 
+// tma_load_2d_pair for a warp-uniform code path: the lane with `leader` != 0 issues.
+__device__ __forceinline__ void tma_load_2d_pair_if(uint32_t leader, uint32_t dst, const CUtensorMap* map, uint32_t mbar,
+                                                    int c0, int c1) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+      "[%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(c0), "r"(c1), "r"(leader)
+      : "memory");
+}
+// umma_pair_commit_if on the barrier at shared-memory address `bar` of both CTAs.
+__device__ __forceinline__ void umma_pair_commit_both_if(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %2, 0;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3)), "r"(leader)
+      : "memory");
+}
+// warp_wait for waits that are short as a rule: the clock is read only after
+// some polls in vain.
+__device__ __forceinline__ bool warp_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait(bar, parity, abort);
+}
+
+// 32 bytes to memory (32-byte aligned).
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // One scale tile (512 B of each CTA's shared memory, at the same offset) into
 // four TMEM columns of each CTA of the pair.
 __device__ __forceinline__ void tmem_copy_scales_pair_if(uint32_t leader, uint32_t taddr, uint64_t sdesc) {
@@ -86,41 +133,77 @@ __device__ __forceinline__ void tmem_copy_scales_pair_if(uint32_t leader, uint32
 
 struct MxLinearParams {
   CUtensorMap x_map;   // bytes [M, row bytes], box 128 x 128, 128B swizzle
-  CUtensorMap w_map;   // bytes [d_out, row bytes], box 128 x 96, 128B swizzle
+  CUtensorMap w_map;   // bytes [d_out, row bytes], box 128 x 128, 128B swizzle
+  CUtensorMap w96_map, w32_map;  // the same, boxes 128 x 96 and 128 x 32
   CUtensorMap xs_map;  // scale tiles as 8-byte words [row blocks, tiles * 64], box (tiles of a stage * 64) x 1
   CUtensorMap ws_map;  // the same of W, box (tiles of a stage * 64) x 2
   const float* bias;   // [d_out] or null
   __nv_bfloat16* Y;    // [M, d_out]
   float alpha;
   int M, row_bytes, d_out, act;
-  int n_tiles, tiles;  // column tiles (192), all tiles
+  int n_tiles, tiles;  // column tiles, all tiles
+  int wide;            // rows of Y are 32-byte aligned
 };
 
-constexpr int kMxTileN = 192;
-constexpr int kMxStages = 6;
-constexpr int kMxABytes = 128 * 128;
-constexpr int kMxBBytes = 96 * 128;
+constexpr int kMxThreads = 640;  // warps 0-3 producers / MMA / TMEM, warps 4-19 epilogue
+constexpr int kMxTileN = 256;
+constexpr int kMxABytes = 128 * 128, kMxBBytes = 128 * 128;
 // scale tiles along a row in a stage: 128 B hold 4 (mxfp8), 8 (mxfp4) or 16 (nvfp4) scales
 __host__ __device__ constexpr int mx_stage_tiles(int fmt) { return fmt == kMxFp8 ? 1 : fmt == kMxFp4 ? 2 : 4; }
 __host__ __device__ constexpr int mx_stage_bytes(int fmt) { return kMxABytes + kMxBBytes + 3 * 512 * mx_stage_tiles(fmt); }
-__host__ __device__ constexpr int mx_linear_smem(int fmt) { return 1024 + kMxStages * mx_stage_bytes(fmt) + 256; }
+constexpr int kMxStages = 5;
+__host__ __device__ constexpr int mx_linear_smem(int fmt) { return 1024 + kMxStages * mx_stage_bytes(fmt) + 16 * 256 + 256; }
+
+// act(alpha v + bias) of a row's next 64 columns (of which `left` exist),
+// rounded to bf16, to memory: stores of 32 bytes (whole sectors) where rows are
+// so aligned, else of 16.
+template <bool kGelu>
+__device__ __forceinline__ void mx_store_row(const uint32_t* v, float alpha, const float4* bias, __nv_bfloat16* y, int left,
+                                             int wide) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {  // 16 columns
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 b = bias[4 * c + k];
+      float f[4] = {fmaf(__uint_as_float(v[16 * c + 4 * k]), alpha, b.x), fmaf(__uint_as_float(v[16 * c + 4 * k + 1]), alpha, b.y),
+                    fmaf(__uint_as_float(v[16 * c + 4 * k + 2]), alpha, b.z),
+                    fmaf(__uint_as_float(v[16 * c + 4 * k + 3]), alpha, b.w)};
+      if constexpr (kGelu) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) f[x] = gelu_tanh_f(f[x]);
+      }
+      w[2 * k] = pack_bf16x2(f[0], f[1]);
+      w[2 * k + 1] = pack_bf16x2(f[2], f[3]);
+    }
+    if (wide) {  // d_out is a multiple of 16
+      if (16 * c < left) st_global32(y + 16 * c, w);
+    } else {
+      if (16 * c < left) *reinterpret_cast<uint4*>(y + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (16 * c + 8 < left) *reinterpret_cast<uint4*>(y + 16 * c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
 
 template <int kFmt>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     mx_linear_pair_kernel(const __grid_constant__ MxLinearParams p) {
   constexpr int ST = kMxStages, KT = mx_stage_tiles(kFmt);
-  constexpr int kSfA = 512 * KT, kSfB = 1024 * KT;
+  constexpr int kSfA = 512 * KT, kSfB = 1024 * KT;  // bytes of a stage's scales
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = sm;
   uint8_t* sB = sA + ST * kMxABytes;
   uint8_t* sSA = sB + ST * kMxBBytes;
   uint8_t* sSB = sSA + ST * kSfA;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sSB + ST * kSfB);  // [ST] both CTAs' stage loaded (rank 0)
+  float* sBias = reinterpret_cast<float*>(sSB + ST * kSfB);       // [16 epilogue warps][64]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sBias + 16 * 64);  // [ST] both CTAs' stage loaded (rank 0)
   uint64_t* empty = full + ST;                                     // [ST] stage consumed
   uint64_t* acc_full = empty + ST;                                 // [2] accumulator complete
   uint64_t* acc_empty = acc_full + 2;                              // [2] accumulator read back (rank 0)
-  uint64_t* drain = acc_empty + 2;                                 // MMA abort path
+  uint64_t* sh_full = acc_empty + 2;                               // the shared columns complete
+  uint64_t* sh_empty = sh_full + 1;                                // the shared columns read back (rank 0)
+  uint64_t* drain = sh_empty + 1;                                  // MMA abort path
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   __shared__ int abort_flag;
 
@@ -128,8 +211,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const int nk = (p.row_bytes + 127) / 128;
   const int pair = static_cast<int>(blockIdx.x >> 1), n_pairs = static_cast<int>(gridDim.x >> 1);
-  // 256 x 192 tiles of this pair: t = pair + i * n_pairs (column tile fastest)
-  const int n_local = p.tiles > pair ? (p.tiles - 1 - pair) / n_pairs + 1 : 0;
+  // 256 x 256 tiles of this pair: t = pair + i * n_pairs (column tile fastest)
+  int n_local = p.tiles > pair ? (p.tiles - 1 - pair) / n_pairs + 1 : 0;
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
@@ -139,8 +222,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&acc_full[a], 1);
-      mbar_init(&acc_empty[a], 512);  // every epilogue thread of both CTAs
+      mbar_init(&acc_empty[a], 24);  // the epilogue warps of both CTAs that read its own columns
     }
+    mbar_init(sh_full, 1);
+    mbar_init(sh_empty, 8);  // the epilogue warps that read them
     mbar_init(drain, 1);
     fence_mbar_init();
   }
@@ -149,40 +234,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   __syncthreads();
   cluster_sync();  // the partner's barriers are initialised before any remote arrival
   tc_fence_after();
-  const uint32_t tbase = *tmem_slot;
+  // All 512 columns are allocated, so they begin at address 0: a constant, and
+  // with it every TMEM address of the issue loop (read from shared memory,
+  // it would pass through a vector register in front of each instruction).
+  constexpr uint32_t tbase = 0;
+  if (*tmem_slot != tbase) {
+    if (threadIdx.x == 0) raise_status(1 << 4);
+    n_local = 0;
+  }
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer (both CTAs)
-    if (lane == 0) {
-      tma_prefetch_desc(&p.x_map);
-      tma_prefetch_desc(&p.w_map);
-      tma_prefetch_desc(&p.xs_map);
-      tma_prefetch_desc(&p.ws_map);
+  if (warp == 0 || warp == 3) {
+    // ------------------------------------------------------------ producers (both CTAs)
+    // warp 0: elements; warp 3: scales. Each loop runs warp-uniformly and one
+    // elected lane issues, so that addresses stay in uniform registers.
+    const uint32_t leader = elect_one_sync();
+    const bool elements = warp == 0;
+    if (leader) {
+      tma_prefetch_desc(elements ? &p.x_map : &p.xs_map);
+      tma_prefetch_desc(elements ? &p.w_map : &p.ws_map);
+      if (elements) {
+        tma_prefetch_desc(&p.w96_map);
+        tma_prefetch_desc(&p.w32_map);
+      }
     }
     const uint32_t full0 = cluster_addr(full, 0);  // the even CTA's stage barriers
-    int issued = 0;
+    const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB), sa0 = smem_u32(sSA), sb0 = smem_u32(sSB);
+    const uint32_t expect = elements && rank == 0 ? leader : 0u;
+    int issued = 0, s = 0;
+    uint32_t wrap = 1;  // parity of the last release of stage s (none in the first round)
     bool ok = true;
     for (int i = 0; i < n_local && ok; ++i) {
       const int t = pair + i * n_pairs, nt = t % p.n_tiles;
       // this CTA's rows and columns; rows past the matrix are zero fill and not stored
       const int r0 = (t / p.n_tiles) * 256 + 128 * static_cast<int>(rank);
-      const int n0 = nt * kMxTileN, nb = n0 + 96 * static_cast<int>(rank);
+      const int n0 = nt * kMxTileN, rk = static_cast<int>(rank);
+      const int own = n0 + (i & 1 ? 64 : 0) + 96 * rk, shared = n0 + (i & 1 ? 0 : 192) + 32 * rk;
       for (int kc = 0; kc < nk; ++kc) {
-        const int g = i * nk + kc, s = g % ST;
-        if (g >= ST && !warp_wait(&empty[s], ((g / ST) - 1) & 1, &abort_flag)) {
+        if (issued >= ST && !warp_wait_short(&empty[s], wrap, &abort_flag)) {
           ok = false;
           break;
         }
-        if (lane == 0) {
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * mx_stage_bytes(kFmt));
-          const uint32_t bar = full0 + static_cast<uint32_t>(s * sizeof(uint64_t));
-          tma_load_2d_pair(sA + s * kMxABytes, &p.x_map, bar, 128 * kc, r0);
-          tma_load_2d_pair(sB + s * kMxBBytes, &p.w_map, bar, 128 * kc, nb);
-          tma_load_2d_pair(sSA + s * kSfA, &p.xs_map, bar, 64 * KT * kc, r0 >> 7);
-          tma_load_2d_pair(sSB + s * kSfB, &p.ws_map, bar, 64 * KT * kc, n0 >> 7);
+        const uint32_t bar = full0 + static_cast<uint32_t>(s * sizeof(uint64_t));
+        if (elements) {
+          if (expect) mbar_arrive_expect_tx(&full[s], 2 * mx_stage_bytes(kFmt));
+          tma_load_2d_pair_if(leader, a0 + s * kMxABytes, &p.x_map, bar, 128 * kc, r0);
+          if (kc == 0 || kc == nk - 1) {
+            tma_load_2d_pair_if(leader, b0 + s * kMxBBytes, &p.w96_map, bar, 128 * kc, own);
+            tma_load_2d_pair_if(leader, b0 + s * kMxBBytes + 96 * 128, &p.w32_map, bar, 128 * kc, shared);
+          } else {
+            tma_load_2d_pair_if(leader, b0 + s * kMxBBytes, &p.w_map, bar, 128 * kc, n0 + 128 * rk);
+          }
+        } else {
+          tma_load_2d_pair_if(leader, sa0 + s * kSfA, &p.xs_map, bar, 64 * KT * kc, r0 >> 7);
+          tma_load_2d_pair_if(leader, sb0 + s * kSfB, &p.ws_map, bar, 64 * KT * kc, n0 >> 7);
         }
-        __syncwarp();
-        issued = g + 1;
+        ++issued;
+        if (++s == ST) {
+          s = 0;
+          wrap ^= 1u;
+        }
       }
     }
     if ((!ok || abort_flag) && lane == 0 && rank == 0) {
@@ -192,9 +302,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
     const uint32_t leader = elect_one_sync();
-    const uint32_t empty0 = cluster_addr(empty, 0), empty1 = cluster_addr(empty, 1);
-    const uint32_t accf0 = cluster_addr(acc_full, 0), accf1 = cluster_addr(acc_full, 1);
+    // descriptors: constant high words, and low words (the address in 16s,
+    // below 2^14 everywhere) that move with the stage
+    constexpr uint64_t kMat = 0xFFFFFFFF00000000ull;
+    const uint64_t dA = make_sdesc(smem_u32(sA), 16, 1024, kSwizzle128B), dB = make_sdesc(smem_u32(sB), 16, 1024, kSwizzle128B);
+    const uint64_t dSA = make_sdesc(smem_u32(sSA), 0, 128, kSwizzleNone), dSB = make_sdesc(smem_u32(sSB), 0, 128, kSwizzleNone);
+    auto at = [&](uint64_t d, uint32_t lo) { return (d & kMat) | lo; };
     const int last_steps = (p.row_bytes - 128 * (nk - 1) + 31) / 32;  // 32-byte steps of the last stage
+    int s = 0;
+    uint32_t round = 0;
+    constexpr uint32_t sfa = tbase + 448, sfb = sfa + 16;
     bool ok = true;
     for (int i = 0; i < n_local && ok; ++i) {
       const int a = i & 1;
@@ -203,47 +320,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t tacc = tbase + kMxTileN * a;
-      // an odd column tile begins 64 rows (two TMEM columns) into its first scale tile
-      const uint32_t sfb_shift = ((pair + i * n_pairs) % p.n_tiles) & 1 ? 2u : 0u;
+      const uint32_t tacc = tbase + 192 * a;
+      const uint32_t down = 64 * a, dshared = 192 * (a ^ 1);  // first columns of the own and of the shared part
       for (int kc = 0; kc < nk; ++kc) {
-        const int g = i * nk + kc, s = g % ST;
-        if (!warp_wait(&full[s], (g / ST) & 1, &abort_flag)) {
+        if (!warp_wait_short(&full[s], round, &abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t a0 = smem_u32(sA + s * kMxABytes), b0 = smem_u32(sB + s * kMxBBytes);
-        const uint32_t sa0 = smem_u32(sSA + s * kSfA), sb0 = smem_u32(sSB + s * kSfB);
-        const uint32_t sfa = tbase + 2 * kMxTileN + 48u * (g & 1), sfb = sfa + 16;
+        const uint32_t la = static_cast<uint32_t>(dA) + s * (kMxABytes >> 4), lb = static_cast<uint32_t>(dB) + s * (kMxBBytes >> 4);
+        const uint32_t lsa = static_cast<uint32_t>(dSA) + s * (kSfA >> 4), lsb = static_cast<uint32_t>(dSB) + s * (kSfB >> 4);
 #pragma unroll
         for (int j = 0; j < KT; ++j) {
-          tmem_copy_scales_pair_if(leader, sfa + 4 * j, make_sdesc(sa0 + 512 * j, 0, 128, kSwizzleNone));
-          tmem_copy_scales_pair_if(leader, sfb + 8 * j, make_sdesc(sb0 + 512 * j, 0, 128, kSwizzleNone));
-          tmem_copy_scales_pair_if(leader, sfb + 8 * j + 4, make_sdesc(sb0 + 512 * (KT + j), 0, 128, kSwizzleNone));
+          tmem_copy_scales_pair_if(leader, sfa + 4 * j, at(dSA, lsa + 32 * j));
+          tmem_copy_scales_pair_if(leader, sfb + 8 * j, at(dSB, lsb + 32 * j));
+          tmem_copy_scales_pair_if(leader, sfb + 8 * j + 4, at(dSB, lsb + 32 * (KT + j)));
         }
         const int steps = kc == nk - 1 ? last_steps : 4;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
+        const uint32_t acc = kc != 0 ? 1u : 0u;
+        auto mma = [&](int kk, uint32_t d, uint32_t b, uint32_t sf, int N) {
           // scale tile and byte of step kk
           constexpr int per = 4 / KT;  // steps that share a tile
           const int j = kk / per, id = kFmt == kMxFp8 ? kk : kFmt == kMxFp4 ? 2 * (kk & 1) : 0;
-          if (kk < steps)
-            umma_pair_mx_if<kFmt>(leader, tacc, make_sdesc(a0 + 32 * kk, 16, 1024, kSwizzle128B),
-                                  make_sdesc(b0 + 32 * kk, 16, 1024, kSwizzle128B),
-                                  make_idesc_mx(kFmt, 256, kMxTileN, id), sfa + 4 * j, sfb + 8 * j + sfb_shift,
-                                  (kc | kk) != 0 ? 1u : 0u);
+          umma_pair_mx_if<kFmt>(kk < steps ? leader : 0u, d, at(dA, la + 2 * kk), at(dB, b + 2 * kk), make_idesc_mx(kFmt, 256, N, id),
+                                sfa + 4 * j, sf + 8 * j, kk != 0 ? 1u : acc);
+        };
+        auto all = [&] {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma(kk, tacc, lb, sfb, 256);
+        };
+        auto own = [&] {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma(kk, tacc + down, lb, sfb + (down >> 5), 192);
+        };
+        auto shared = [&] {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma(kk, tacc + dshared, lb + (96 * 128 >> 4), sfb + (dshared >> 5), 64);
+        };
+        auto shared_read = [&] {  // the last tile's shared columns have been read
+          ok = i == 0 || warp_wait_short(sh_empty, (i - 1) & 1, &abort_flag);
+          tc_fence_after();
+          return ok;
+        };
+        if (kc == nk - 1) {
+          if (kc == 0 && !shared_read()) break;
+          shared();
+          umma_pair_commit_both_if(leader, smem_u32(sh_full));
+          own();
+        } else if (kc == 0) {
+          own();
+          if (!shared_read()) break;
+          shared();
+        } else {
+          all();
         }
         // both CTAs' stage may be refilled once these copies and MMAs have read it
-        const uint32_t so = static_cast<uint32_t>(s * sizeof(uint64_t));
-        umma_pair_commit_if(leader, empty0 + so);
-        umma_pair_commit_if(leader, empty1 + so);
+        umma_pair_commit_both_if(leader, smem_u32(&empty[s]));
+        if (++s == ST) {
+          s = 0;
+          round ^= 1u;
+        }
       }
-      if (ok) {
-        const uint32_t ao = static_cast<uint32_t>(a * sizeof(uint64_t));
-        umma_pair_commit_if(leader, accf0 + ao);
-        umma_pair_commit_if(leader, accf1 + ao);
-      }
+      if (ok) umma_pair_commit_both_if(leader, smem_u32(&acc_full[a]));
     }
     if (!ok) {
       // wait for every MMA the leader issued before TMEM is released
@@ -253,51 +391,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue (both CTAs)
-    // warp 4 + 4e + q: TMEM lanes 32q .. 32q + 31, columns 96e .. 96e + 95
-    const int q = warp & 3, row = q * 32 + lane, e = (warp - 4) >> 2;
-    const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
-    const uint32_t acce0 = cluster_addr(acc_empty, 0);
+    // warp 4 + 4e + q: TMEM lanes 32q .. 32q + 31, columns 64e .. 64e + 63;
+    // each lane stores its row's 128 bytes
+    const int q = warp & 3, e = (warp - 4) >> 2;
+    const uint32_t lane_addr = tbase + (static_cast<uint32_t>(q * 32) << 16) + 64 * e;
+    const uint32_t acce0 = cluster_addr(acc_empty, 0), she0 = cluster_addr(sh_empty, 0);
+    const float4* bias = reinterpret_cast<const float4*>(sBias + 64 * (warp - 4));
+    float2* bias2 = reinterpret_cast<float2*>(sBias + 64 * (warp - 4));
+    bias2[lane] = make_float2(0.f, 0.f);
     for (int i = 0; i < n_local; ++i) {
-      const int a = i & 1;
-      if (!warp_wait(&acc_full[a], (i >> 1) & 1, &abort_flag)) break;
+      const int a = i & 1, t = pair + i * n_pairs;
+      const int nc = (t % p.n_tiles) * kMxTileN + 64 * e;
+      const int r = (t / p.n_tiles) * 256 + 128 * static_cast<int>(rank) + 32 * q + lane;
+      __syncwarp();  // the last tile's bias has been read
+      if (p.bias != nullptr && nc + 2 * lane < p.d_out)  // d_out is a multiple of 8
+        bias2[lane] = make_float2(__ldg(p.bias + nc + 2 * lane), __ldg(p.bias + nc + 2 * lane + 1));
+      const bool sh = e == (a ? 0 : 3);
+      if (!(sh ? warp_wait_short(sh_full, i & 1, &abort_flag) : warp_wait_short(&acc_full[a], (i >> 1) & 1, &abort_flag))) break;
       tc_fence_after();
-      const int t = pair + i * n_pairs, n0 = (t % p.n_tiles) * kMxTileN;
-      const int r = (t / p.n_tiles) * 256 + 128 * static_cast<int>(rank) + row;
-      const bool valid = r < p.M;
-      __nv_bfloat16* yrow = p.Y + static_cast<size_t>(valid ? r : 0) * p.d_out;
-#pragma unroll 1
-      for (int c = 3 * e; c < 3 * e + 3; ++c) {
-        uint32_t v[32];
-        tmem_ld32(tbase + lane_addr + kMxTileN * a + 32 * c, v);
-        tmem_ld_wait32(v);
-        if (c == 3 * e + 2) {
-          // the accumulator is released to the even CTA's issuer
-          tc_fence_before();
-          mbar_arrive_cluster(acce0 + static_cast<uint32_t>(a * sizeof(uint64_t)));
-        }
-        const int nc = n0 + 32 * c;
-        if (nc >= p.d_out) continue;
-        uint32_t pk[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          float f0 = __uint_as_float(v[2 * k]) * p.alpha, f1 = __uint_as_float(v[2 * k + 1]) * p.alpha;
-          if (p.bias != nullptr && nc + 2 * k < p.d_out) {  // d_out is even
-            f0 += __ldg(p.bias + nc + 2 * k);
-            f1 += __ldg(p.bias + nc + 2 * k + 1);
-          }
-          if (p.act == 1) {
-            f0 = gelu_tanh_f(f0);
-            f1 = gelu_tanh_f(f1);
-          }
-          pk[k] = pack_bf16x2(f0, f1);
-        }
-        if (valid) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (nc + 8 * u < p.d_out)
-              *reinterpret_cast<uint4*>(yrow + nc + 8 * u) =
-                  make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
-        }
+      uint32_t v[64];
+      tmem_ld32(lane_addr + 192 * a, v);
+      tmem_ld32(lane_addr + 192 * a + 32, v + 32);
+      tmem_ld_wait32(v);
+      tmem_ld_wait32(v + 32);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(sh ? she0 : acce0 + static_cast<uint32_t>(a * sizeof(uint64_t)));
+      if (r < p.M) {
+        __nv_bfloat16* y = p.Y + static_cast<size_t>(r) * p.d_out + nc;
+        if (p.act == 1) mx_store_row<true>(v, p.alpha, bias, y, p.d_out - nc, p.wide);
+        else mx_store_row<false>(v, p.alpha, bias, y, p.d_out - nc, p.wide);
       }
     }
   }
@@ -306,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   __syncthreads();
   cluster_sync();  // the partner's MMAs, copies and arrivals are done
   tc_fence_after();
-  if (warp == 2) tmem_dealloc_pair(tbase, 512);
+  if (warp == 2) tmem_dealloc_pair(*tmem_slot, 512);
 }
 
 }  // namespace safe

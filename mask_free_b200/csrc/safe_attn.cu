@@ -616,7 +616,9 @@ safe_status launch_mx_linear(MxLinearParams& p, const void* X, const void* Xs, c
   constexpr int smem = mx_linear_smem(kFmt), words = 64 * mx_stage_tiles(kFmt);
   const uint64_t ct = static_cast<uint64_t>(mx_tiles(d_in, kFmt)) * 64, rb = static_cast<uint64_t>(p.row_bytes);
   if (!encode_bytes_map(&p.x_map, X, false, rb, static_cast<uint64_t>(p.M), 128, 128) ||
-      !encode_bytes_map(&p.w_map, W, false, rb, static_cast<uint64_t>(p.d_out), 128, 96) ||
+      !encode_bytes_map(&p.w_map, W, false, rb, static_cast<uint64_t>(p.d_out), 128, 128) ||
+      !encode_bytes_map(&p.w96_map, W, false, rb, static_cast<uint64_t>(p.d_out), 128, 96) ||
+      !encode_bytes_map(&p.w32_map, W, false, rb, static_cast<uint64_t>(p.d_out), 128, 32) ||
       !encode_bytes_map(&p.xs_map, Xs, true, ct, static_cast<uint64_t>((p.M + 127LL) / 128), words, 1) ||
       !encode_bytes_map(&p.ws_map, Ws, true, ct, static_cast<uint64_t>((p.d_out + 127) / 128), words, 2))
     return SAFE_ERR_CUDA;
@@ -625,9 +627,9 @@ safe_status launch_mx_linear(MxLinearParams& p, const void* X, const void* Xs, c
   if (tiles > INT_MAX) return SAFE_ERR_UNSUPPORTED;
   p.tiles = static_cast<int>(tiles);
   if (!allow_smem<mx_linear_pair_kernel<kFmt>>(smem)) return SAFE_ERR_CUDA;
-  const int mp = resident_pairs<mx_linear_pair_kernel<kFmt>>(kLinThreads, smem);
+  const int mp = resident_pairs<mx_linear_pair_kernel<kFmt>>(kMxThreads, smem);
   const int pairs = static_cast<int>(tiles < mp ? tiles : mp);
-  mx_linear_pair_kernel<kFmt><<<2 * pairs, kLinThreads, smem, s>>>(p);
+  mx_linear_pair_kernel<kFmt><<<2 * pairs, kMxThreads, smem, s>>>(p);
   return launch_status();
 }
 
@@ -1235,6 +1237,7 @@ safe_status safe_mx_linear(const void* X, const void* X_scales, const void* Wt, 
   MxLinearParams p{};
   p.bias = bias;
   p.Y = static_cast<__nv_bfloat16*>(Y);
+  p.wide = d_out % 16 == 0 && aligned_to(Y, 32);
   p.alpha = alpha;
   p.M = static_cast<int>(rows);
   p.row_bytes = row_bytes;
