@@ -415,7 +415,8 @@ safe_status safe_rope(const void* q, const int64_t q_strides[3], void* oq, const
                       void* stream);
 
 /*
- * Microscaled rows. A matrix [rows, D] (D a multiple of 32) keeps one scale for
+ * Microscaled rows. A matrix [rows, D] (D a multiple of 32, quantised and decoded
+ * up to 2^20) keeps one scale for
  * each block of consecutive elements of a row:
  *   SAFE_MXFP8  e4m3 elements, blocks of 32, power-of-two scales (e8m0)
  *   SAFE_MXFP4  e2m1 elements, blocks of 32, power-of-two scales (e8m0)

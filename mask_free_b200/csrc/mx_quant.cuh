@@ -37,6 +37,7 @@ struct Raw8<__nv_bfloat16> {
   uint4 a;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
   __device__ __forceinline__ void get(float* v) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -51,6 +52,7 @@ struct Raw8<__half> {
   uint4 a;
   __device__ __forceinline__ void load(const __half* p) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void store(__half* p) const { *reinterpret_cast<uint4*>(p) = a; }
   __device__ __forceinline__ void get(float* v) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -69,6 +71,10 @@ struct Raw8<float> {
     b = reinterpret_cast<const float4*>(p)[1];
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
   __device__ __forceinline__ void get(float* v) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -90,6 +96,51 @@ __device__ __forceinline__ void store8(__half* p, const float* v) {
 __device__ __forceinline__ void store8(float* p, const float* v) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+// 16 elements, in accesses of 32 bytes where `wide` (the address is so aligned):
+// a warp's 16-byte accesses 32 bytes apart would touch every sector twice.
+__device__ __forceinline__ void ld_global32(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p));
+}
+__device__ __forceinline__ void st_global32(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void load16(Raw8<T>* r, const T* x, int wide) {
+  if (wide) {
+    if constexpr (sizeof(T) == 2) {
+      ld_global32(x, r[0].a, r[1].a);
+    } else {
+      ld_global32(x, reinterpret_cast<uint4&>(r[0].a), reinterpret_cast<uint4&>(r[0].b));
+      ld_global32(x + 8, reinterpret_cast<uint4&>(r[1].a), reinterpret_cast<uint4&>(r[1].b));
+    }
+  } else {
+    r[0].load(x);
+    r[1].load(x + 8);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const __nv_bfloat16*, const float* v) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ uint4 pack8(const __half*, const float* v) {
+  return make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
+}
+template <typename T>
+__device__ __forceinline__ void store16(T* y, const float* v, int wide) {
+  if (!wide) {
+    store8(y, v);
+    store8(y + 8, v + 8);
+  } else if constexpr (sizeof(T) == 2) {
+    st_global32(y, pack8(y, v), pack8(y, v + 8));
+  } else {
+    const uint4* u = reinterpret_cast<const uint4*>(v);
+    st_global32(y, u[0], u[1]);
+    st_global32(y + 8, u[2], u[3]);
+  }
 }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
@@ -201,6 +252,42 @@ __device__ __forceinline__ uint32_t nvfp4_elements(const float* v, float s, floa
   return lo;
 }
 
+// Largest magnitude of 16 loaded elements as the bits of an fp32 number
+// (16-bit magnitudes order as their bits do, infinities and NaN on top).
+__device__ __forceinline__ uint32_t amax16_bits(const uint4& a, const uint4& b) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+  return max(m & 0xffffu, m >> 16);
+}
+__device__ __forceinline__ uint32_t amax16(const Raw8<__nv_bfloat16>& a, const Raw8<__nv_bfloat16>& b, const float*) {
+  return amax16_bits(a.a, b.a) << 16;
+}
+__device__ __forceinline__ uint32_t amax16(const Raw8<__half>& a, const Raw8<__half>& b, const float*) {
+  return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(amax16_bits(a.a, b.a)))));
+}
+__device__ __forceinline__ uint32_t amax16(const Raw8<float>&, const Raw8<float>&, const float* v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+  return m;
+}
+
+// ---------------------------------------------------------------- rows in groups of 128
+// Quotient by a divisor fixed at launch, for u < 2^31: with l = ceil(log2 d) and
+// m = ceil(2^(31 + l) / d), u / d = (u m) >> (31 + l); d >= 2.
+struct FastDiv {
+  uint32_t m, s;
+  __device__ __forceinline__ uint32_t div(uint32_t u) const { return __umulhi(u, m) >> s; }
+};
+
+// A thread of both kernels below takes one unit of 16 consecutive elements of
+// four rows, 32 apart: their scales share 16 bytes of a tile, so that scales
+// move in whole 16-byte words, and four loads are in flight. Position t of the
+// grid is unit t % upr of rows (t / upr) / 32 * 128 + (t / upr) % 32 + 32 i.
+constexpr int kMxRows = 4;
+
 // ---------------------------------------------------------------- quantisation of rows
 struct MxQuantParams {
   const void* X;      // [B, N, D]
@@ -208,56 +295,57 @@ struct MxQuantParams {
   uint8_t* data;      // [B * R, D or D / 2]
   uint8_t* scales;    // tiles
   float g, inv6g;
-  int B, N, R, D;
+  int N, R, D;
   int ct;             // scale tiles along a row
-  int upr;            // 16-element units of a row, a multiple of 4 (those past D only fill the scale tiles up)
-  long long rows;     // B * R
-  long long rows_pad; // up to a multiple of 128
+  int upr;            // 16-element units of a row, up to whole scale tiles
+  int rows, row0;     // B * R; the launch's first row
+  uint32_t threads;   // positions of the launch
+  int wide;           // X is 32-byte aligned
+  FastDiv by_upr, by_R;
 };
 
-// Thread = one unit of 16 consecutive elements: a whole block of nvfp4, half of
-// one of 32. Bound by memory: x is read once, the elements and scales are
-// written once.
-constexpr int kMxUnroll = 4;
+// Bound by memory: x is read once, elements and scales are written once.
+// Measured (bf16, 51200 x 2304): mxfp8 59 us, mxfp4 52 us, nvfp4 61 us (6.0,
+// 5.7, 4.9 TB/s). A thread for one unit of one row, with 64-bit divisions for
+// its place, took 72, 70 and 82 us.
 template <typename T, int kFmt>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(const MxQuantParams p) {
-  const long long total = p.rows_pad * p.upr;
-  const long long u0 = static_cast<long long>(blockIdx.x) * (256 * kMxUnroll) + threadIdx.x;
-  Raw8<T> raw[kMxUnroll][2];
-  long long row[kMxUnroll];
-  int unit[kMxUnroll];
+  const uint32_t t = blockIdx.x * 256 + threadIdx.x;
+  // the grid's last positions past the end repeat the last one, without stores
+  const bool live = t < p.threads;
+  const uint32_t tt = live ? t : p.threads - 1, rr = p.by_upr.div(tt);
+  const int unit = static_cast<int>(tt - rr * p.upr);
+  const int r0 = p.row0 + static_cast<int>((rr >> 5) * 128 + (rr & 31));
+  const bool in = unit * 16 < p.D;
+  Raw8<T> raw[kMxRows][2];
 #pragma unroll
-  for (int i = 0; i < kMxUnroll; ++i) {
-    const long long u = u0 + 256 * i;
+  for (int i = 0; i < kMxRows; ++i) {
+    const int row = r0 + 32 * i;
     raw[i][0].zero();
     raw[i][1].zero();
-    row[i] = u < total ? u / p.upr : -1;
-    unit[i] = static_cast<int>(u - row[i] * p.upr);
-    if (row[i] >= 0 && row[i] < p.rows && unit[i] * 16 < p.D) {
-      long long src = row[i];
+    if (in && row < p.rows) {
+      long long src = row;
       if (p.S != nullptr) {
-        int idx = __ldg(p.S + row[i]);
+        int idx = __ldg(p.S + row);
         if (idx < 0 || idx >= p.N) {
-          if (unit[i] == 0) raise_status(1 << 5);
+          if (unit == 0 && live) raise_status(1 << 5);
           idx = 0;
         }
-        src = (row[i] / p.R) * p.N + idx;
+        src = (p.R == 1 ? row : static_cast<long long>(p.by_R.div(row))) * p.N + idx;
       }
-      const T* x = static_cast<const T*>(p.X) + src * p.D + unit[i] * 16;
-      raw[i][0].load(x);
-      raw[i][1].load(x + 8);
+      const T* x = static_cast<const T*>(p.X) + src * p.D + unit * 16;
+      load16(raw[i], x, p.wide);
     }
   }
+  constexpr int kLanes = kFmt == kNvFp4 ? 4 : 8;  // lanes whose scales make a word: 4 scales of one row
+  uint32_t words[kMxRows];
 #pragma unroll
-  for (int i = 0; i < kMxUnroll; ++i) {
-    // every lane takes the shuffles; lanes of four hold 64 elements of one row
+  for (int i = 0; i < kMxRows; ++i) {
+    const int row = r0 + 32 * i;
     float v[16];
     raw[i][0].get(v);
     raw[i][1].get(v + 8);
-    uint32_t amax = 0;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) amax = max(amax, __float_as_uint(v[e]) & 0x7fffffffu);
-    uint32_t byte, out[4];
+    uint32_t amax = amax16(raw[i][0], raw[i][1], v), byte, out[4];
     if constexpr (kFmt == kNvFp4) {
       byte = nvfp4_scale(amax, p.g, p.inv6g);
       const float s = e4m3_value(byte);
@@ -277,25 +365,22 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const MxQuantParams p)
           out[e] = e4m3x4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv, v[4 * e + 3] * inv);
       }
     }
-    // the scale bytes of the four lanes: four of nvfp4 (one word), two of the others (half a word)
-    if (unit[i] * 16 >= p.D || row[i] >= p.rows) byte = 0;
-    uint32_t word = byte << (8 * (threadIdx.x & 3));
-    if constexpr (kFmt != kNvFp4) word = byte << (8 * ((threadIdx.x & 3) >> 1));
-    word |= __shfl_xor_sync(0xffffffffu, word, 1);
+    // this row's word of scales; those past the row or the matrix are zero
+    const int at = kFmt == kNvFp4 ? threadIdx.x & 3 : (threadIdx.x >> 1) & 3;
+    uint32_t word = in && row < p.rows ? byte << (8 * at) : 0u;
+    if constexpr (kFmt == kNvFp4) word |= __shfl_xor_sync(0xffffffffu, word, 1);
     word |= __shfl_xor_sync(0xffffffffu, word, 2);
-    if (row[i] < 0) continue;
-    if ((threadIdx.x & 3) == 0) {
-      if constexpr (kFmt == kNvFp4)
-        *reinterpret_cast<uint32_t*>(p.scales + mx_scale_at(row[i], unit[i], p.ct)) = word;
+    if constexpr (kFmt != kNvFp4) word |= __shfl_xor_sync(0xffffffffu, word, 4);
+    words[i] = word;
+    if (live && in && row < p.rows) {
+      if constexpr (kFmt == kMxFp8)
+        *reinterpret_cast<uint4*>(p.data + static_cast<size_t>(row) * p.D + unit * 16) = make_uint4(out[0], out[1], out[2], out[3]);
       else
-        *reinterpret_cast<uint16_t*>(p.scales + mx_scale_at(row[i], unit[i] >> 1, p.ct)) = static_cast<uint16_t>(word);
+        *reinterpret_cast<uint2*>(p.data + static_cast<size_t>(row) * (p.D / 2) + unit * 8) = make_uint2(out[0], out[1]);
     }
-    if (row[i] >= p.rows || unit[i] * 16 >= p.D) continue;
-    if constexpr (kFmt == kMxFp8)
-      *reinterpret_cast<uint4*>(p.data + row[i] * p.D + unit[i] * 16) = make_uint4(out[0], out[1], out[2], out[3]);
-    else
-      *reinterpret_cast<uint2*>(p.data + row[i] * (p.D / 2) + unit[i] * 8) = make_uint2(out[0], out[1]);
   }
+  if (live && (threadIdx.x & (kLanes - 1)) == 0)
+    *reinterpret_cast<uint4*>(p.scales + mx_scale_at(r0, unit / (kLanes / 4), p.ct)) = make_uint4(words[0], words[1], words[2], words[3]);
 }
 
 // ---------------------------------------------------------------- decoding
@@ -304,49 +389,73 @@ struct MxDecodeParams {
   const uint8_t* scales;
   void* Y;  // [rows, D]
   float g;
-  int D, ct, upr;  // upr = D / 16
-  long long units;
+  int D, ct, upr, rows, row0;  // upr = D / 16
+  int wide;                    // Y is 32-byte aligned
+  uint32_t threads;
+  FastDiv by_upr;
 };
 
 // value = element * scale * g: the product of element and scale is exact in
 // fp32, the factor g rounds once, the conversion to the output type once.
+// Bound by memory. Measured (to bf16, 51200 x 2304): mxfp8 59 us, mxfp4 and
+// nvfp4 51 us (5.8 - 6.0 TB/s); with stores of 16 bytes, two to a sector, 68 and
+// 70 us.
 template <typename T, int kFmt>
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxDecodeParams p) {
-  const long long u = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  if (u >= p.units) return;
-  const long long row = u / p.upr;
-  const int unit = static_cast<int>(u - row * p.upr);
-  float v[16], s;
-  if constexpr (kFmt == kNvFp4)
-    s = e4m3_value(p.scales[mx_scale_at(row, unit, p.ct)]);
-  else
-    s = e8m0_value(p.scales[mx_scale_at(row, unit >> 1, p.ct)]);
-  if constexpr (kFmt == kMxFp8) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p.data + row * p.D + unit * 16);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  const uint32_t t = blockIdx.x * 256 + threadIdx.x;
+  if (t >= p.threads) return;
+  const uint32_t rr = p.by_upr.div(t);
+  const int unit = static_cast<int>(t - rr * p.upr);
+  const int r0 = p.row0 + static_cast<int>((rr >> 5) * 128 + (rr & 31));
+  const int j = kFmt == kNvFp4 ? unit : unit >> 1;
+  const uint4 sw = __ldg(reinterpret_cast<const uint4*>(p.scales + mx_scale_at(r0, j & ~3, p.ct)));
+  const uint32_t words[4] = {sw.x, sw.y, sw.z, sw.w};
+  uint4 raw[kMxRows];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t h2;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)))));
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  } else {
-    const uint2 a = *reinterpret_cast<const uint2*>(p.data + row * (p.D / 2) + unit * 8);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      // e2m1: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 by their twofold in four bits each
-      const uint32_t c = ((i < 8 ? a.x : a.y) >> (4 * (i & 7))) & 15u;
-      const float m = 0.5f * static_cast<float>((0xC8643210u >> (4 * (c & 7u))) & 15u);
-      v[i] = c & 8u ? -m : m;
+  for (int i = 0; i < kMxRows; ++i) {
+    const int row = r0 + 32 * i;
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (row < p.rows) {
+      if constexpr (kFmt == kMxFp8) {
+        raw[i] = __ldg(reinterpret_cast<const uint4*>(p.data + static_cast<size_t>(row) * p.D + unit * 16));
+      } else {
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(p.data + static_cast<size_t>(row) * (p.D / 2) + unit * 8));
+        raw[i].x = a.x;
+        raw[i].y = a.y;
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = v[i] * s * p.g;
-  T* y = static_cast<T*>(p.Y) + row * p.D + unit * 16;
-  store8(y, v);
-  store8(y + 8, v + 8);
+  for (int i = 0; i < kMxRows; ++i) {
+    const int row = r0 + 32 * i;
+    if (row >= p.rows) break;
+    const uint32_t byte = (words[i] >> (8 * (j & 3))) & 0xffu;
+    const float s = kFmt == kNvFp4 ? e4m3_value(byte) : e8m0_value(byte);
+    float v[16];
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {  // two elements
+      uint32_t h2;
+      if constexpr (kFmt == kMxFp8) {
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)))));
+      } else {
+        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+            "mov.b32 {b0, b1, b2, b3}, %1;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
+            : "=r"(h2)
+            : "r"(w[e / 4] >> (8 * (e & 3))));
+      }
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+      v[2 * e] = f.x * s;
+      v[2 * e + 1] = f.y * s;
+      if constexpr (kFmt == kNvFp4) {
+        v[2 * e] *= p.g;
+        v[2 * e + 1] *= p.g;
+      }
+    }
+    T* y = static_cast<T*>(p.Y) + static_cast<size_t>(row) * p.D + unit * 16;
+    store16(y, v, p.wide);
+  }
 }
 
 }  // namespace safe

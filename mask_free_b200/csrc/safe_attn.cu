@@ -481,6 +481,7 @@ bool apart(const View4& s, const View4& t, size_t e) {
   }
   return false;
 }
+constexpr int kMxMaxD = 1 << 20;  // keeps the positions of 128 rows below 2^31
 int mx_block(int fmt) { return fmt == SAFE_NVFP4 ? 16 : 32; }
 // Scale tiles along a row of D elements.
 int mx_tiles(int D, int fmt) { return (D / mx_block(fmt) + 3) / 4; }
@@ -545,32 +546,89 @@ safe_status launch_norm(const NormParams& p, bool vec, cudaStream_t s) {
 }
 
 template <typename T>
-void launch_rope(const RopeParams& p, bool pairs, bool vec, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>((p.rows + kRopeWarps - 1) / kRopeWarps);
-  const size_t smem = static_cast<size_t>(kRopeWarps) * ((p.r / 2 + 3) & ~3) * sizeof(float2);
-  if (pairs) {
-    if (vec) rope_kernel<T, true, true><<<grid, 32 * kRopeWarps, smem, s>>>(p);
-    else rope_kernel<T, true, false><<<grid, 32 * kRopeWarps, smem, s>>>(p);
-  } else {
-    if (vec) rope_kernel<T, false, true><<<grid, 32 * kRopeWarps, smem, s>>>(p);
-    else rope_kernel<T, false, false><<<grid, 32 * kRopeWarps, smem, s>>>(p);
+safe_status launch_rope(RopeParams& p, bool pairs, bool vec, cudaStream_t s) {
+  constexpr int U = sizeof(T) == 2 ? 2 : 1;  // heads in flight for each lane
+  if (vec) {
+    // The ring for heads side by side in their rows and more tokens than its
+    // CTAs take at once, from 4 KB a token in 16 bits: 51200 tokens of 24 + 24
+    // heads of 96 take 152 us against 186 with plain loads, those of 8 + 2
+    // heads of 128 (2.5 KB) 80 against 59. In fp32 lines are full either way:
+    // 319 against 299 us.
+    if constexpr (sizeof(T) == 2) {
+      const size_t token = static_cast<size_t>(p.t[0].H + p.t[1].H) * p.d * sizeof(T);
+      bool ring = token >= 4096 && token <= kRopeBulkMax;
+      for (const RopeTensor& t : p.t) ring = ring && (t.H <= 1 || (t.xh == p.d && t.oh == p.d));
+      const size_t smem = kRopeStages * ((token + 127) / 128 * 128) + p.r * sizeof(float2) + kRopeStages * sizeof(uint64_t);
+      const size_t per_sm = 220 * 1024 / (smem + 1024) < 8 ? 220 * 1024 / (smem + 1024) : 8;
+      const unsigned ctas = static_cast<unsigned>(per_sm * device_sms());
+      if (ring && p.rows >= 2 * ctas) {
+        constexpr int limit = kRopeStages * kRopeBulkMax + 1024 * sizeof(float2) + 256;
+        if (!(pairs ? allow_smem<rope_bulk_kernel<T, true>>(limit) : allow_smem<rope_bulk_kernel<T, false>>(limit)))
+          return SAFE_ERR_CUDA;
+        if (pairs) rope_bulk_kernel<T, true><<<ctas, 128, smem, s>>>(p);
+        else rope_bulk_kernel<T, false><<<ctas, 128, smem, s>>>(p);
+        return launch_status();
+      }
+    }
+    // few tokens: as few warps for each as take its heads in one batch (2458
+    // tokens of 24 + 24 heads: 14.3 us against 18.4 with one warp); many: one
+    const int per = p.r / 16, batch = U * (per < 32 ? 32 / per : 1), H = p.t[0].H + p.t[1].H;
+    p.warps = H <= batch || p.rows > 32u * device_sms() ? 1 : H <= 2 * batch ? 2 : 4;
+    const unsigned tokens = kRopeWarps / p.warps, grid = (p.rows + tokens - 1) / tokens;
+    const size_t cs = static_cast<size_t>(tokens) * (p.r / 2) * sizeof(float2);
+    if (pairs) rope_vec_kernel<T, true, U><<<grid, 32 * kRopeWarps, cs, s>>>(p);
+    else rope_vec_kernel<T, false, U><<<grid, 32 * kRopeWarps, cs, s>>>(p);
+    return launch_status();
   }
-}
-
-template <typename T>
-safe_status launch_mx_quantize(const MxQuantParams& p, int fmt, unsigned blocks, cudaStream_t s) {
-  if (fmt == SAFE_MXFP8) mx_quantize_kernel<T, kMxFp8><<<blocks, 256, 0, s>>>(p);
-  else if (fmt == SAFE_MXFP4) mx_quantize_kernel<T, kMxFp4><<<blocks, 256, 0, s>>>(p);
-  else mx_quantize_kernel<T, kNvFp4><<<blocks, 256, 0, s>>>(p);
+  const unsigned grid = (p.rows + kRopeWarps - 1) / kRopeWarps;
+  const size_t smem = static_cast<size_t>(kRopeWarps) * (p.r / 2) * sizeof(float2);
+  if (pairs) rope_kernel<T, true><<<grid, 32 * kRopeWarps, smem, s>>>(p);
+  else rope_kernel<T, false><<<grid, 32 * kRopeWarps, smem, s>>>(p);
   return launch_status();
 }
 
+FastDiv fast_div(uint32_t d) {  // d >= 2
+  uint32_t l = 1;
+  while ((1ull << l) < d) ++l;
+  return FastDiv{static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), l - 1};
+}
+
+// Calls launch(first row, rows, positions) over slices of whole 128-row groups
+// whose positions (a quarter of the rows times upr) stay below 2^31.
+template <typename F>
+safe_status mx_slices(int64_t rows, int upr, F launch) {
+  const int64_t groups = (rows + 127) / 128, per = ((1ll << 31) - 256) / (32ll * upr);
+  for (int64_t g = 0; g < groups; g += per) {
+    const int64_t n = groups - g < per ? groups - g : per;
+    launch(static_cast<int>(128 * g), static_cast<uint32_t>(n * 32 * upr));
+    const safe_status st = launch_status();
+    if (st != SAFE_OK) return st;
+  }
+  return SAFE_OK;
+}
+
 template <typename T>
-safe_status launch_mx_dequantize(const MxDecodeParams& p, int fmt, unsigned blocks, cudaStream_t s) {
-  if (fmt == SAFE_MXFP8) mx_dequantize_kernel<T, kMxFp8><<<blocks, 256, 0, s>>>(p);
-  else if (fmt == SAFE_MXFP4) mx_dequantize_kernel<T, kMxFp4><<<blocks, 256, 0, s>>>(p);
-  else mx_dequantize_kernel<T, kNvFp4><<<blocks, 256, 0, s>>>(p);
-  return launch_status();
+safe_status launch_mx_quantize(MxQuantParams& p, int fmt, cudaStream_t s) {
+  return mx_slices(p.rows, p.upr, [&](int row0, uint32_t threads) {
+    p.row0 = row0;
+    p.threads = threads;
+    const unsigned blocks = (threads + 255) / 256;
+    if (fmt == SAFE_MXFP8) mx_quantize_kernel<T, kMxFp8><<<blocks, 256, 0, s>>>(p);
+    else if (fmt == SAFE_MXFP4) mx_quantize_kernel<T, kMxFp4><<<blocks, 256, 0, s>>>(p);
+    else mx_quantize_kernel<T, kNvFp4><<<blocks, 256, 0, s>>>(p);
+  });
+}
+
+template <typename T>
+safe_status launch_mx_dequantize(MxDecodeParams& p, int fmt, cudaStream_t s) {
+  return mx_slices(p.rows, p.upr, [&](int row0, uint32_t threads) {
+    p.row0 = row0;
+    p.threads = threads;
+    const unsigned blocks = (threads + 255) / 256;
+    if (fmt == SAFE_MXFP8) mx_dequantize_kernel<T, kMxFp8><<<blocks, 256, 0, s>>>(p);
+    else if (fmt == SAFE_MXFP4) mx_dequantize_kernel<T, kMxFp4><<<blocks, 256, 0, s>>>(p);
+    else mx_dequantize_kernel<T, kNvFp4><<<blocks, 256, 0, s>>>(p);
+  });
 }
 
 // 2-D matrix [outer, inner] of bytes or 8-byte words (row pitch = inner); rows
@@ -1110,7 +1168,7 @@ safe_status safe_rope(const void* q, const int64_t q_strides[3], void* oq, const
   if (sum != r / 2) return SAFE_ERR_INVALID_ARG;
   if (!aligned_to(freq, 8) || !aligned_to(pos, 4) || !aligned_to(S, 4)) return SAFE_ERR_INVALID_ARG;
   RopeParams p{};
-  bool vec = d % 8 == 0 && (interleaved ? r % 8 == 0 : r % 16 == 0);
+  bool vec = d % 8 == 0 && r % 16 == 0;
   const void* xs[2] = {q, k};
   void* os[2] = {oq, ok};
   const int64_t* st[4] = {q_strides, oq_strides, k_strides, ok_strides};
@@ -1150,14 +1208,13 @@ safe_status safe_rope(const void* q, const int64_t q_strides[3], void* oq, const
   p.d = d;
   p.r = r;
   p.m = m;
-  p.rows = static_cast<long long>(B) * R;  // <= B N <= INT_MAX
+  p.rows = static_cast<uint32_t>(B) * R;  // <= B N <= INT_MAX
   cudaStream_t s = as_stream(stream);
   switch (dtype) {
-    case SAFE_F32: launch_rope<float>(p, interleaved != 0, vec, s); break;
-    case SAFE_F16: launch_rope<__half>(p, interleaved != 0, vec, s); break;
-    default: launch_rope<__nv_bfloat16>(p, interleaved != 0, vec, s);
+    case SAFE_F32: return launch_rope<float>(p, interleaved != 0, vec, s);
+    case SAFE_F16: return launch_rope<__half>(p, interleaved != 0, vec, s);
+    default: return launch_rope<__nv_bfloat16>(p, interleaved != 0, vec, s);
   }
-  return launch_status();
 }
 
 safe_status safe_mx_quantize(const void* X, int dtype, const int32_t* S, int k, int fmt, float g, void* data,
@@ -1166,6 +1223,7 @@ safe_status safe_mx_quantize(const void* X, int dtype, const int32_t* S, int k, 
   if (!aligned16(X) || !aligned16(data) || !aligned16(scales) || !aligned_to(S, 4)) return SAFE_ERR_INVALID_ARG;
   if (!sizes_ok(B, N, 1) || (S != nullptr && (k < 1 || k > N)) || D < 32 || D % 32 != 0) return SAFE_ERR_INVALID_ARG;
   if (!mx_factor_ok(fmt, g)) return SAFE_ERR_INVALID_ARG;
+  if (D > kMxMaxD) return SAFE_ERR_UNSUPPORTED;
   MxQuantParams p{};
   p.X = X;
   p.S = S;
@@ -1173,23 +1231,22 @@ safe_status safe_mx_quantize(const void* X, int dtype, const int32_t* S, int k, 
   p.scales = static_cast<uint8_t*>(scales);
   p.g = g;
   p.inv6g = 1.f / (6.f * g);
-  p.B = B;
   p.N = N;
   p.R = S != nullptr ? k : N;
   p.D = D;
   p.ct = mx_tiles(D, fmt);
   p.upr = p.ct * 4 * (fmt == SAFE_NVFP4 ? 1 : 2);
-  p.rows = static_cast<long long>(B) * p.R;
-  p.rows_pad = (p.rows + 127) / 128 * 128;
+  p.rows = B * p.R;  // <= B N <= INT_MAX
+  p.wide = aligned_to(X, 32);
+  p.by_upr = fast_div(static_cast<uint32_t>(p.upr));
+  p.by_R = fast_div(static_cast<uint32_t>(p.R > 1 ? p.R : 2));
   const size_t db = static_cast<size_t>(p.rows) * (fmt == SAFE_MXFP8 ? D : D / 2);
   const size_t sb = safe_mx_scale_bytes(p.rows, D, fmt), xb = static_cast<size_t>(B) * N * D * float_size(dtype);
   if (overlap(data, db, X, xb) || overlap(scales, sb, X, xb) || overlap(data, db, scales, sb)) return SAFE_ERR_INVALID_ARG;
-  const long long blocks = (p.rows_pad * p.upr + 256 * kMxUnroll - 1) / (256 * kMxUnroll);
-  if (blocks > INT_MAX) return SAFE_ERR_UNSUPPORTED;
   switch (dtype) {
-    case SAFE_F32: return launch_mx_quantize<float>(p, fmt, static_cast<unsigned>(blocks), as_stream(stream));
-    case SAFE_F16: return launch_mx_quantize<__half>(p, fmt, static_cast<unsigned>(blocks), as_stream(stream));
-    default: return launch_mx_quantize<__nv_bfloat16>(p, fmt, static_cast<unsigned>(blocks), as_stream(stream));
+    case SAFE_F32: return launch_mx_quantize<float>(p, fmt, as_stream(stream));
+    case SAFE_F16: return launch_mx_quantize<__half>(p, fmt, as_stream(stream));
+    default: return launch_mx_quantize<__nv_bfloat16>(p, fmt, as_stream(stream));
   }
 }
 
@@ -1198,6 +1255,7 @@ safe_status safe_mx_dequantize(const void* data, const void* scales, int fmt, fl
   if (float_size(dtype) == 0) return SAFE_ERR_UNSUPPORTED;
   if (!aligned16(data) || !aligned16(scales) || !aligned16(Y)) return SAFE_ERR_INVALID_ARG;
   if (rows < 1 || rows > INT_MAX || D < 32 || D % 32 != 0 || !mx_factor_ok(fmt, g)) return SAFE_ERR_INVALID_ARG;
+  if (D > kMxMaxD) return SAFE_ERR_UNSUPPORTED;
   const size_t db = static_cast<size_t>(rows) * (fmt == SAFE_MXFP8 ? D : D / 2);
   const size_t yb = static_cast<size_t>(rows) * D * float_size(dtype);
   if (overlap(Y, yb, data, db) || overlap(Y, yb, scales, safe_mx_scale_bytes(rows, D, fmt))) return SAFE_ERR_INVALID_ARG;
@@ -1209,13 +1267,13 @@ safe_status safe_mx_dequantize(const void* data, const void* scales, int fmt, fl
   p.D = D;
   p.ct = mx_tiles(D, fmt);
   p.upr = D / 16;
-  p.units = static_cast<long long>(rows) * p.upr;
-  const long long blocks = (p.units + 255) / 256;
-  if (blocks > INT_MAX) return SAFE_ERR_UNSUPPORTED;
+  p.rows = static_cast<int>(rows);
+  p.wide = aligned_to(Y, 32);
+  p.by_upr = fast_div(static_cast<uint32_t>(p.upr));
   switch (dtype) {
-    case SAFE_F32: return launch_mx_dequantize<float>(p, fmt, static_cast<unsigned>(blocks), as_stream(stream));
-    case SAFE_F16: return launch_mx_dequantize<__half>(p, fmt, static_cast<unsigned>(blocks), as_stream(stream));
-    default: return launch_mx_dequantize<__nv_bfloat16>(p, fmt, static_cast<unsigned>(blocks), as_stream(stream));
+    case SAFE_F32: return launch_mx_dequantize<float>(p, fmt, as_stream(stream));
+    case SAFE_F16: return launch_mx_dequantize<__half>(p, fmt, as_stream(stream));
+    default: return launch_mx_dequantize<__nv_bfloat16>(p, fmt, as_stream(stream));
   }
 }
 

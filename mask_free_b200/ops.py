@@ -524,17 +524,44 @@ _i64x3 = ctypes.c_int64 * 3
 def _run(name: str, dev: torch.device, *args):
     """Call entry point `name` on `dev` (which need not be the current device)
     with that device's current stream as the last argument."""
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            st = getattr(lib(), name)(*args, _stream())
+    fn, idx = getattr(lib(), name), dev.index
+    if idx is None:
+        st = fn(*args, _stream())
+    elif idx == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(idx))
     else:
-        st = getattr(lib(), name)(*args, _stream())
+        with torch.cuda.device(idx):
+            st = fn(*args, _raw_stream(idx))
     if st != SAFE_OK:
         raise SafeError(name, st)
 
 
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same number without a Stream object around it (3 us of a small call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
+
+
+def _check_tensor(t, name: str, dtype, shape, dev):
+    """_need for a known shape on a known device, quick when all is well."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
+        _need(t, name, dtype, len(shape), shape, dev)
+
+
+def _out_like(t, name: str, like, dtype, shape):
+    """An output buffer on the device of `like`: new, or the given one checked."""
+    if t is not None:
+        _check_tensor(t, name, dtype, shape, like.device)
+        return t
+    if dtype is like.dtype and like.shape == shape and like.is_contiguous():
+        return torch.empty_like(like)
+    return like.new_empty(shape, dtype=dtype)
 
 
 def _float_code(t, name: str) -> int:
@@ -547,11 +574,11 @@ def _rows_of(S, B: int, N: int, dev) -> int:
     """Rows of each sample: N, or k of S [B, k] (checked)."""
     if S is None:
         return N
-    _need(S, "S", torch.int32, 2, device=dev)
-    k = S.shape[1]
-    if S.shape[0] != B or not 1 <= k <= N:
+    if not (isinstance(S, torch.Tensor) and S.dtype is torch.int32 and S.device == dev and S.is_contiguous()):
+        _need(S, "S", torch.int32, 2, device=dev)
+    if S.dim() != 2 or S.shape[0] != B or not 1 <= S.shape[1] <= N:
         raise ValueError(f"S must have shape ({B}, 1..{N}), got {tuple(S.shape)}")
-    return k
+    return S.shape[1]
 
 
 class MxTensor:
@@ -560,9 +587,10 @@ class MxTensor:
     `scales` the scale bytes in tiles of 128 rows x 4 (flat uint8, the rows of
     data's leading dims one after another; layout: safe_mx_quantize in
     include/safe_attn.h), `fmt` "mxfp8", "mxfp4" or "nvfp4", and `scale` the
-    factor of the whole matrix (nvfp4; 1 otherwise)."""
+    factor of the whole matrix (nvfp4; 1 otherwise). Checked once, here: its
+    parts cannot be exchanged afterwards."""
 
-    __slots__ = ("data", "scales", "fmt", "scale")
+    __slots__ = ("_data", "_scales", "_fmt", "_scale")
 
     def __init__(self, data: torch.Tensor, scales: torch.Tensor, fmt: str, scale: float = 1.0):
         if fmt not in _FORMATS:
@@ -570,10 +598,16 @@ class MxTensor:
         want = torch.float8_e4m3fn if fmt == "mxfp8" else torch.uint8
         if not isinstance(data, torch.Tensor) or data.dim() < 2:
             raise ValueError("data must be a tensor of at least 2 dims")
-        _need(data, "data", want, data.dim())
+        if not (_on_device(data) and data.dtype is want and data.is_contiguous()):
+            _need(data, "data", want, data.dim())
         rows, D = _mx_rows(data, fmt)
-        _need(scales, "scales", torch.uint8, 1, (mx_scale_bytes(rows, D, fmt),), data.device)
-        self.data, self.scales, self.fmt, self.scale = data, scales, fmt, _factor(fmt, scale)
+        _check_tensor(scales, "scales", torch.uint8, (mx_scale_bytes(rows, D, fmt),), data.device)
+        self._data, self._scales, self._fmt, self._scale = data, scales, fmt, _factor(fmt, scale)
+
+    data = property(lambda self: self._data)
+    scales = property(lambda self: self._scales)
+    fmt = property(lambda self: self._fmt)
+    scale = property(lambda self: self._scale)
 
     @property
     def shape(self) -> Tuple[int, ...]:
@@ -603,25 +637,19 @@ def mx_scale_bytes(rows: int, D: int, fmt: str) -> int:
     return -(-rows // 128) * -(-D // (64 if fmt == "nvfp4" else 128)) * 512
 
 
-def _mx_new(lead, D: int, fmt: str, scale: float, dev) -> MxTensor:
-    """A microscaled matrix [*lead, D] of undefined contents."""
-    m = MxTensor.__new__(MxTensor)  # made to fit: nothing to check
-    rows = math.prod(lead)
-    if fmt == "mxfp8":
-        m.data = torch.empty((*lead, D), dtype=torch.float8_e4m3fn, device=dev)
-    else:
-        m.data = torch.empty((*lead, D // 2), dtype=torch.uint8, device=dev)
-    m.scales = torch.empty(mx_scale_bytes(rows, D, fmt), dtype=torch.uint8, device=dev)
-    m.fmt, m.scale = fmt, float(scale)
-    return m
-
-
-def _mx_out(out, lead, D: int, fmt: str, scale: float, dev) -> MxTensor:
+def _mx_out(out, lead, D: int, fmt: str, scale: float, like) -> MxTensor:
+    """A microscaled matrix [*lead, D] on the device of `like`: one of undefined
+    contents, or the given one checked."""
     if out is None:
-        return _mx_new(lead, D, fmt, scale, dev)
-    if not isinstance(out, MxTensor) or out.fmt != fmt or out.shape != (*lead, D) or out.device != dev:
-        raise ValueError(f"out must be an MxTensor {fmt} of shape {(*lead, D)} on {dev}")
-    out.scale = float(scale)
+        m = MxTensor.__new__(MxTensor)  # made to fit: nothing to check
+        m._data = like.new_empty((*lead, D) if fmt == "mxfp8" else (*lead, D // 2),
+                                 dtype=torch.float8_e4m3fn if fmt == "mxfp8" else torch.uint8)
+        m._scales = like.new_empty(mx_scale_bytes(math.prod(lead), D, fmt), dtype=torch.uint8)
+        m._fmt, m._scale = fmt, scale
+        return m
+    if not isinstance(out, MxTensor) or out.fmt != fmt or out.shape != (*lead, D) or out.device != like.device:
+        raise ValueError(f"out must be an MxTensor {fmt} of shape {(*lead, D)} on {like.device}")
+    out._scale = scale
     return out
 
 
@@ -638,40 +666,47 @@ def rms_norm(x, w=None, residual=None, S=None, eps=1e-6, x_compact=False, quant=
     update: h is the residual itself, its rows (of S, strictly ascending, or
     all) updated in place. out, h: buffers for the results."""
     dt = _float_code(x, "x")
-    _need(x, "x", x.dtype, 3)
-    dev = x.device
-    src = x if residual is None else residual
-    if residual is not None:
-        _need(residual, "residual", x.dtype, 3, device=dev)
-    B, N, D = src.shape
-    k = 0
-    if residual is None and S is not None and x_compact:
-        raise ValueError("x_compact needs a residual: the rows of S are already gathered in x")
-    R = _rows_of(S, B, N, dev)
-    if S is not None:
-        k = R
-    full = S is not None and not x_compact
-    _need(x, "x", x.dtype, 3, (B, N if full else R, D), dev)
+    if not _on_device(x) or x.dim() != 3:
+        _need(x, "x", x.dtype, 3)
+    dev, dtype = x.device, x.dtype
+    if residual is not None and (not isinstance(residual, torch.Tensor) or residual.dim() != 3):
+        _need(residual, "residual", dtype, 3, device=dev)
+    B, N, D = x.shape if residual is None else residual.shape
+    k, full = 0, False
+    if S is None:
+        R = N
+    else:
+        if residual is None and x_compact:
+            raise ValueError("x_compact needs a residual: the rows of S are already gathered in x")
+        R = k = _rows_of(S, B, N, dev)
+        full = not x_compact
+    _check_tensor(x, "x", dtype, (B, N if full else R, D), dev)
     if w is not None:
-        _need(w, "w", torch.float32, 1, (D,), dev)
-    if quant not in (None, "mxfp8"):
-        raise ValueError(f"quant must be None or 'mxfp8', got {quant!r}")
-    if (update or h is not None) and residual is None:
-        raise ValueError("update and h need a residual")
-    if update and h is not None:
-        raise ValueError("update writes the sums to the residual: h must be None")
-    if residual is not None:
-        h = residual if update else _out(h, "h", x.dtype, (B, R, D), dev)
+        _check_tensor(w, "w", torch.float32, (D,), dev)
+    shape = (B, R, D)
+    if residual is None:
+        if update or h is not None:
+            raise ValueError("update and h need a residual")
+    else:
+        _check_tensor(residual, "residual", dtype, (B, N, D), dev)
+        if not update:
+            h = _out_like(h, "h", x, dtype, shape)
+        elif h is not None:
+            raise ValueError("update writes the sums to the residual: h must be None")
+        else:
+            h = residual
     if quant is None:
-        y = _out(out, "out", x.dtype, (B, R, D), dev)
+        y = _out_like(out, "out", x, dtype, shape)
         yp, qp, sp = y.data_ptr(), None, None
     else:
+        if quant != "mxfp8":
+            raise ValueError(f"quant must be None or 'mxfp8', got {quant!r}")
         if D % 32:
             raise ValueError(f"an 8-bit output needs D a multiple of 32, got {D}")
-        y = _mx_out(out, (B, R), D, quant, 1.0, dev)
+        y = _mx_out(out, (B, R), D, quant, 1.0, x)
         yp, qp, sp = None, y.data.data_ptr(), y.scales.data_ptr()
     _run("safe_rms_norm", dev, x.data_ptr(), 1 if full else 0, _ptr(residual), _ptr(S), k, _ptr(w), eps, _ptr(h),
-         1 if update and S is not None else 0, yp, qp, sp, dt, B, N, D)
+         1 if update and k else 0, yp, qp, sp, dt, B, N, D)
     return y if residual is None else (y, h)
 
 
@@ -680,7 +715,7 @@ class RopeTable:
     int64 in 2^-64 turns, `sections` the pairs of each position axis, `m` the
     factor on the rotated elements."""
 
-    __slots__ = ("freq", "sections", "m", "r", "_sections")
+    __slots__ = ("freq", "sections", "m", "r", "_sections", "_freq_ptr")
 
     def __init__(self, freq: torch.Tensor, sections: Sequence[int], m: float = 1.0):
         _need(freq, "freq", torch.int64, 1)
@@ -692,6 +727,7 @@ class RopeTable:
             raise ValueError(f"m must be finite, got {m}")
         self.freq, self.m = freq, float(m)
         self._sections = (ctypes.c_int32 * len(self.sections))(*self.sections)
+        self._freq_ptr = ctypes.cast(freq.data_ptr(), _i64p)
 
 
 def rope_frequencies(r: int, base: float = 10000.0, sections: Optional[Sequence[int]] = None, kind: str = "none",
@@ -747,15 +783,15 @@ def rope_table(r: int, base: float = 10000.0, sections: Optional[Sequence[int]] 
 
 def _heads(t, name: str, dtype, B, R, d, dev):
     """Check a [B, R, H, d] tensor or view (contiguous in d); returns H, strides."""
-    if not isinstance(t, torch.Tensor) or not _on_device(t) or t.device != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise ValueError(f"{name} must be a tensor on {dev}")
     shape = t.shape
-    if t.dtype != dtype or len(shape) != 4 or shape[0] != B or shape[1] != R or shape[2] < 1 or shape[3] != d:
+    if t.dtype is not dtype or len(shape) != 4 or shape[0] != B or shape[1] != R or shape[2] < 1 or shape[3] != d:
         raise ValueError(f"{name} must be {dtype} of shape ({B}, {R}, heads, {d}), got {t.dtype} {tuple(shape)}")
-    st = t.stride()
-    if st[3] != 1:
+    b, n, h, one = t.stride()
+    if one != 1:
         raise ValueError(f"{name} must be contiguous in its last dim")
-    return shape[2], _i64x3(st[0], st[1], st[2])
+    return shape[2], _i64x3(b, n, h)
 
 
 def rope(q, k, table: RopeTable, pos=None, S=None, interleaved=False, inplace=False, out=None):
@@ -764,45 +800,47 @@ def rope(q, k, table: RopeTable, pos=None, S=None, interleaved=False, inplace=Fa
     (fp32, fp16 or bf16; views of a fused projection too, contiguous in the
     last dim). pos: int32 [N, axes] shared by the samples (one axis: [N] will
     do) or [B, N, axes]; None: the token index. S [B, R] int32: row r is token
-    S[b, r], else token r. interleaved: pairs
-    (2i, 2i + 1) instead of (i, i + r / 2). Returns (q, k) turned: new
-    contiguous tensors, those of out=(q, k), or with inplace q and k
-    themselves."""
+    S[b, r], else token r. interleaved: pairs (2i, 2i + 1) instead of
+    (i, i + r / 2). Returns (q, k) turned: new contiguous tensors, those of
+    out=(q, k), or with inplace q and k themselves."""
     dt = _float_code(q, "q")
     if not isinstance(table, RopeTable):
         raise ValueError("table must be a RopeTable")
-    if q.dim() != 4:
-        raise ValueError(f"q must have 4 dims, got {tuple(q.shape)}")
+    if not _on_device(q) or q.dim() != 4:
+        raise ValueError(f"q must be a CUDA tensor of 4 dims, got {tuple(q.shape)} on {q.device}")
     B, R, _, d = q.shape
-    dev, axes = q.device, len(table.sections)
-    H, qs = _heads(q, "q", q.dtype, B, R, d, dev)
-    Hk, ks, oks = 0, None, None
+    dev, dtype, axes, r = q.device, q.dtype, len(table.sections), table.r
+    H, qs = _heads(q, "q", dtype, B, R, d, dev)
+    Hk, ks, kp = 0, None, None
     if k is not None:
-        Hk, ks = _heads(k, "k", q.dtype, B, R, d, dev)
+        Hk, ks = _heads(k, "k", dtype, B, R, d, dev)
+        kp = k.data_ptr()
     if table.freq.device != dev:
         raise ValueError(f"table must be on {dev}")
-    if table.r > d:
-        raise ValueError(f"the table turns {table.r} elements, heads have {d}")
-    N, batched = R, 0
+    if r > d:
+        raise ValueError(f"the table turns {r} elements, heads have {d}")
+    N, batched, pp, sp = R, 0, None, None
     if pos is None:
         if axes != 1:
             raise ValueError(f"a table of {axes} axes needs pos")
         if S is not None:
             raise ValueError("S needs pos (the positions of all tokens)")
     else:
-        nd = pos.dim()
-        if nd == 1 and axes == 1:
-            N, want = pos.shape[0], None
-        elif nd in (2, 3):
-            batched, N = nd - 2, pos.shape[-2]
-            want = (B, N, axes) if batched else (N, axes)
+        if not isinstance(pos, torch.Tensor) or not 1 <= pos.dim() <= 3 or (pos.dim() == 1 and axes != 1):
+            raise ValueError(f"pos must be a tensor [tokens, {axes}] or [{B}, tokens, {axes}]")
+        shape = pos.shape
+        if len(shape) == 1:
+            N = shape[0]
         else:
-            raise ValueError(f"pos must be [tokens, {axes}] or [{B}, tokens, {axes}], got {tuple(pos.shape)}")
-        _need(pos, "pos", torch.int32, nd, want, dev)
+            batched, N = len(shape) - 2, shape[-2]
+            shape = (B, N, axes) if batched else (N, axes)
+        _check_tensor(pos, "pos", torch.int32, shape, dev)
+        pp = pos.data_ptr()
     if S is not None:
-        _need(S, "S", torch.int32, 2, (B, R), dev)
+        _check_tensor(S, "S", torch.int32, (B, R), dev)
         if R > N:
             raise ValueError(f"S names {R} rows of {N} tokens")
+        sp = S.data_ptr()
     elif N != R:
         raise ValueError(f"pos has {N} tokens, q {R} rows")
     if inplace:
@@ -811,31 +849,33 @@ def rope(q, k, table: RopeTable, pos=None, S=None, interleaved=False, inplace=Fa
         oq, ok, oqs, oks = q, k, qs, ks
     else:
         oq, ok = (None, None) if out is None else out
+        oks = None
         if oq is None:
-            oq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            oq = _out_like(None, "", q, dtype, q.shape)
             oqs = _i64x3(R * H * d, H * d, d)
         else:
-            n, oqs = _heads(oq, "out[0]", q.dtype, B, R, d, dev)
+            n, oqs = _heads(oq, "out[0]", dtype, B, R, d, dev)
             if n != H:
                 raise ValueError(f"out[0] must have {H} heads, got {n}")
         if k is None:
             if ok is not None:
                 raise ValueError("out[1] needs k")
         elif ok is None:
-            ok = torch.empty(k.shape, dtype=q.dtype, device=dev)
+            ok = _out_like(None, "", k, dtype, k.shape)
             oks = _i64x3(R * Hk * d, Hk * d, d)
         else:
-            n, oks = _heads(ok, "out[1]", q.dtype, B, R, d, dev)
+            n, oks = _heads(ok, "out[1]", dtype, B, R, d, dev)
             if n != Hk:
                 raise ValueError(f"out[1] must have {Hk} heads, got {n}")
-    _run("safe_rope", dev, q.data_ptr(), qs, oq.data_ptr(), oqs, H, _ptr(k), ks, _ptr(ok), oks, Hk, dt,
-         table.freq.data_ptr(), table._sections, axes, _ptr(pos), batched, _ptr(S), B, N, R, d, table.r,
-         1 if interleaved else 0, table.m)
+    _run("safe_rope", dev, q.data_ptr(), qs, oq.data_ptr(), oqs, H, kp, ks, None if k is None else ok.data_ptr(), oks, Hk, dt,
+         table._freq_ptr, table._sections, axes, pp, batched, sp, B, N, R, d, r, 1 if interleaved else 0, table.m)
     return oq, ok
 
 
 def _factor(fmt: str, scale: float) -> float:
     """The factor of a microscaled matrix as the fp32 number that is kept."""
+    if scale == 1.0:
+        return 1.0
     s = ctypes.c_float(scale).value
     if fmt == "nvfp4" and not 2.0 ** -100 <= s <= 2.0 ** 100:
         raise ValueError(f"scale must lie in [2^-100, 2^100], got {scale}")
@@ -850,22 +890,25 @@ def mx_quantize(x, fmt: str, S=None, scale: float = 1.0, out=None) -> MxTensor:
     scale: the factor of an nvfp4 matrix (largest magnitude / 2688 lets every
     block scale be represented). Returns an MxTensor [B, k or N, D]."""
     dt = _float_code(x, "x")
-    if fmt not in _FORMATS:
+    code = _FORMATS.get(fmt)
+    if code is None:
         raise ValueError(f"fmt must be one of {sorted(_FORMATS)}, got {fmt!r}")
     nd = x.dim()
     if nd not in (2, 3):
         raise ValueError(f"x must have 2 or 3 dims, got {tuple(x.shape)}")
-    _need(x, "x", x.dtype, nd)
+    if not (_on_device(x) and x.is_contiguous()):
+        _need(x, "x", x.dtype, nd)
     B, N, D = x.shape if nd == 3 else (1, *x.shape)
     if D < 32 or D % 32:
         raise ValueError(f"rows must have a multiple of 32 elements, got {D}")
-    dev, g = x.device, _factor(fmt, scale)
-    if S is not None and nd == 2:
-        raise ValueError("S needs x of 3 dims")
-    R = _rows_of(S, B, N, dev)
-    m = _mx_out(out, (B, R) if nd == 3 else (N,), D, fmt, g, dev)
-    _run("safe_mx_quantize", dev, x.data_ptr(), dt, _ptr(S), R if S is not None else 0, _FORMATS[fmt], g,
-         m.data.data_ptr(), m.scales.data_ptr(), B, N, D)
+    dev, g, k = x.device, _factor(fmt, scale), 0
+    R = N
+    if S is not None:
+        if nd == 2:
+            raise ValueError("S needs x of 3 dims")
+        R = k = _rows_of(S, B, N, dev)
+    m = _mx_out(out, (B, R) if nd == 3 else (N,), D, fmt, g, x)
+    _run("safe_mx_quantize", dev, x.data_ptr(), dt, _ptr(S), k, code, g, m.data.data_ptr(), m.scales.data_ptr(), B, N, D)
     return m
 
 
@@ -877,7 +920,7 @@ def mx_dequantize(m: MxTensor, dtype=torch.bfloat16, out=None):
         raise ValueError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
     rows, D = _mx_rows(m.data, m.fmt)
     dev = m.device
-    out = _out(out, "out", dtype, (*m.data.shape[:-1], D), dev)
+    out = _out_like(out, "out", m.scales, dtype, (*m.data.shape[:-1], D))
     _run("safe_mx_dequantize", dev, m.data.data_ptr(), m.scales.data_ptr(), _FORMATS[m.fmt], m.scale, out.data_ptr(),
          _FLOATS[dtype], rows, D)
     return out
@@ -898,13 +941,13 @@ def mx_linear(X: MxTensor, W: MxTensor, bias=None, act="none", out=None):
     if W.data.dim() != 2 or dw != d_in or W.device != dev:
         raise ValueError(f"W must be [d_out, {d_in}] on {dev}, got {W.shape} on {W.device}")
     if bias is not None:
-        _need(bias, "bias", torch.float32, 1, (d_out,), dev)
+        _check_tensor(bias, "bias", torch.float32, (d_out,), dev)
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
     alpha = X.scale * W.scale
     if not 2.0 ** -126 <= abs(alpha) < 2.0 ** 128:
         raise ValueError(f"the product of the operands' factors is out of range: {alpha}")
-    out = _out(out, "out", torch.bfloat16, (*X.data.shape[:-1], d_out), dev)
+    out = _out_like(out, "out", X.scales, torch.bfloat16, (*X.data.shape[:-1], d_out))
     _run("safe_mx_linear", dev, X.data.data_ptr(), X.scales.data_ptr(), W.data.data_ptr(), W.scales.data_ptr(),
          _FORMATS[X.fmt], alpha, _ptr(bias), _ACTS[act], out.data_ptr(), rows, d_in, d_out)
     return out
