@@ -387,8 +387,9 @@ safe_status safe_rms_norm(const void* x, int x_full, const void* res, const int3
  *   (a, b) -> m (a cos - b sin, b cos + a sin)
  * with (a, b) = elements (i, i + r/2), or (2i, 2i + 1) when interleaved.
  *  q, k   device [B, R, H, d] with element strides {sample, row, head} in
- *         *_strides (host, >= 0; the head dim is contiguous), so views of a
- *         fused q, k, v projection are taken as they are. k may be NULL (then
+ *         *_strides (host, >= 0; the head dim is contiguous; NULL: a
+ *         contiguous tensor), so views of a fused q, k, v projection are
+ *         taken as they are. k may be NULL (then
  *         ok NULL, Hk 0). Hq and Hk need not be equal.
  *  oq, ok device, the results, with strides of their own. Each is its input
  *         itself (same strides: in place) or shares no element with the
@@ -466,12 +467,19 @@ safe_status safe_mx_dequantize(const void* data, const void* scales, int fmt, fl
  *  bias  device fp32 [d_out] (4-byte aligned) or NULL; act as
  *        safe_gather_linear (0 = none, 1 = tanh-GELU).
  *  Y     device bf16 [rows, d_out] (written; apart from the operands).
+ *  ws    device workspace of safe_mx_linear_workspace_bytes bytes (32-byte
+ *        aligned; caller-owned, contents undefined after the call) or NULL:
+ *        with it, the tiles of the last, partial wave of CTAs are computed in
+ *        pieces along d_in and added by a second kernel (fp32, in a fixed
+ *        order). The size is 0 where that does not pay off; without it, or
+ *        with less, every tile is computed whole.
  *  d_in >= 64 a multiple of 32, d_out >= 8 a multiple of 8; all pointers but
  *  bias 16-byte aligned.
  */
+size_t safe_mx_linear_workspace_bytes(int64_t rows, int d_in, int d_out, int fmt);
 safe_status safe_mx_linear(const void* X, const void* X_scales, const void* Wt, const void* Wt_scales, int fmt,
                            float alpha, const float* bias, int act, void* Y, int64_t rows, int d_in, int d_out,
-                           void* stream);
+                           void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Device status word: synchronises `stream`, writes to *h_status (host) the

@@ -24,14 +24,17 @@
 // each CTA holds 96 + 32 rows of W, its halves of the two parts, instead of
 // 128: the columns' order stays that of the rows of W.)
 //
-// What bounds it: a stage is 38 KB into shared memory and 38 KB out of it for
-// 512 cycles of MMA, and 1000 W: at K = 9216 nvfp4 runs at 6.1 PFLOP/s with
-// the clock down to 1.45 GHz (mxfp8 2.9 at 1.25 GHz). Measured before: tiles
-// of 192 columns with accumulators apart, 4.2 / 4.9 PFLOP/s (K = 2304 / 9216,
-// nvfp4, 51200 and 12800 x 6912) against 4.8 / 6.1 of these; accumulators that
-// overlap without the split, 4.6 / 5.6 (the tensor core idles 1100 cycles
-// at each tile); the output through shared memory and tiled stores, 4.4 - 4.6
-// at K = 2304 (its 128 KB compete with the operands) against 4.8.
+// What bounds it: a stage is 34 - 38 KB into shared memory and as much out of
+// it for 512 cycles of MMA, and 1000 W. A call by itself (PFLOP/s; 51200 rows at
+// d_in = 2304, 12800 at 9216, d_out 6912): nvfp4 5.1 and 6.2, mxfp4 5.3 and 6.5,
+// mxfp8 3.05 and 2.85, with clocks down to 1.45 and 1.25 GHz; calls back to
+// back, when power sets the clock: nvfp4 3.9 and 4.9, mxfp8 2.3 and 2.25.
+// Measured on the way (nvfp4, d_in 2304 / 9216): tiles of 192 columns with
+// accumulators apart 4.2 / 4.9; accumulators that overlap without the split
+// 4.6 / 5.6 (the tensor core idles 1100 cycles at each tile); the output
+// through shared memory and tiled stores, which compete with the operands,
+// 4.9 / 5.8; a release instead of a relaxed arrival for the accumulator
+// 4.8 / 6.1.
 #pragma once
 
 #include "linear.cuh"
@@ -95,6 +98,12 @@ __device__ __forceinline__ void tma_load_2d_pair_if(uint32_t leader, uint32_t ds
       "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(c0), "r"(c1), "r"(leader)
       : "memory");
 }
+// mbar_arrive_cluster without its release: for a barrier that only hands tensor
+// memory back, which the arriving warp has read (tcgen05.wait::ld). A
+// release waits for the warp's stores of the last tile, 1100 cycles here.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t caddr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
+}
 // umma_pair_commit_if on the barrier at shared-memory address `bar` of both CTAs.
 __device__ __forceinline__ void umma_pair_commit_both_if(uint32_t leader, uint32_t bar) {
   asm volatile(
@@ -113,6 +122,21 @@ __device__ __forceinline__ bool warp_wait_short(uint64_t* bar, uint32_t parity, 
   return warp_wait(bar, parity, abort);
 }
 
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if one of them is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // 32 bytes to memory (32-byte aligned).
 __device__ __forceinline__ void st_global32(void* p, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
@@ -131,6 +155,8 @@ __device__ __forceinline__ void tmem_copy_scales_pair_if(uint32_t leader, uint32
       : "memory");
 }
 
+constexpr int kMxPieces = 96;  // pieces at most
+
 struct MxLinearParams {
   CUtensorMap x_map;   // bytes [M, row bytes], box 128 x 128, 128B swizzle
   CUtensorMap w_map;   // bytes [d_out, row bytes], box 128 x 128, 128B swizzle
@@ -141,8 +167,18 @@ struct MxLinearParams {
   __nv_bfloat16* Y;    // [M, d_out]
   float alpha;
   int M, row_bytes, d_out, act;
-  int n_tiles, tiles;  // column tiles, all tiles
+  int n_tiles;         // column tiles
   int wide;            // rows of Y are 32-byte aligned
+  // Units of work: the first `whole` tiles, then pieces along d_in of the other
+  // tiles, whose sums go to `part` [piece][256][256] fp32. A table, not a
+  // division: its entries are uniform constants to the compiler, as all
+  // operands of the issue loop have to be. (Where it cannot prove that, it
+  // guards every MMA, copy and barrier instruction against lanes that
+  // disagree, and the loop costs more than the MMAs: 313 us instead of 262,
+  // nvfp4, 12800 x 9216 x 6912.)
+  int whole, units;
+  float* part;
+  uint16_t piece_tile[kMxPieces], piece_k0[kMxPieces], piece_n[kMxPieces];  // tile, first stage, stages
 };
 
 constexpr int kMxThreads = 640;  // warps 0-3 producers / MMA / TMEM, warps 4-19 epilogue
@@ -151,8 +187,26 @@ constexpr int kMxABytes = 128 * 128, kMxBBytes = 128 * 128;
 // scale tiles along a row in a stage: 128 B hold 4 (mxfp8), 8 (mxfp4) or 16 (nvfp4) scales
 __host__ __device__ constexpr int mx_stage_tiles(int fmt) { return fmt == kMxFp8 ? 1 : fmt == kMxFp4 ? 2 : 4; }
 __host__ __device__ constexpr int mx_stage_bytes(int fmt) { return kMxABytes + kMxBBytes + 3 * 512 * mx_stage_tiles(fmt); }
-constexpr int kMxStages = 5;
-__host__ __device__ constexpr int mx_linear_smem(int fmt) { return 1024 + kMxStages * mx_stage_bytes(fmt) + 16 * 256 + 256; }
+// As many stages as fit (5 of nvfp4, 6 of the others).
+__host__ __device__ constexpr int mx_stages(int fmt) { return (227 * 1024 - 1024 - 16 * 256 - 256) / mx_stage_bytes(fmt); }
+__host__ __device__ constexpr int mx_linear_smem(int fmt) { return 1024 + mx_stages(fmt) * mx_stage_bytes(fmt) + 16 * 256 + 256; }
+
+// GELU in its tanh form of two values: x / (1 + 2^t), t = x (c1 + c2 x^2) with
+// c1 = -2 sqrt(2 / pi) / ln 2 and c2 = 0.044715 c1 (see gelu_tanh_f); one
+// reciprocal serves both, 1 / a = b / (a b). Below -7.4, where the result is
+// below 2^-55, x is cut off, so that t < 59 and a b is finite; a NaN stays in
+// its own factor x and out of t, which the other value shares.
+// The exp unit bounds this epilogue: 3 of its operations for two values instead
+// of 4 (nvfp4, 12800 x 2304 x 9216: 131 -> 127 us).
+__device__ __forceinline__ void gelu_tanh_2(float& x0, float& x1) {
+  const uint64_t x = f2_pack(fmaxf(x0, -7.4f), fmaxf(x1, -7.4f)), c2 = f2_pack(-0.10294324f, -0.10294324f), c1 = f2_pack(-2.3022082f, -2.3022082f);
+  float t0, t1, a, b;
+  f2_unpack(f2_mul(x, f2_fma(f2_mul(x, x), c2, c1)), t0, t1);
+  f2_unpack(f2_add(f2_pack(ex2_approx(t0), ex2_approx(t1)), f2_pack(1.f, 1.f)), a, b);
+  const float r = rcp_approx(a * b);
+  x0 = max_nan(x0, -7.4f) * (r * b);
+  x1 = max_nan(x1, -7.4f) * (r * a);
+}
 
 // act(alpha v + bias) of a row's next 64 columns (of which `left` exist),
 // rounded to bf16, to memory: stores of 32 bytes (whole sectors) where rows are
@@ -170,8 +224,8 @@ __device__ __forceinline__ void mx_store_row(const uint32_t* v, float alpha, con
                     fmaf(__uint_as_float(v[16 * c + 4 * k + 2]), alpha, b.z),
                     fmaf(__uint_as_float(v[16 * c + 4 * k + 3]), alpha, b.w)};
       if constexpr (kGelu) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) f[x] = gelu_tanh_f(f[x]);
+        gelu_tanh_2(f[0], f[1]);
+        gelu_tanh_2(f[2], f[3]);
       }
       w[2 * k] = pack_bf16x2(f[0], f[1]);
       w[2 * k + 1] = pack_bf16x2(f[2], f[3]);
@@ -188,7 +242,7 @@ __device__ __forceinline__ void mx_store_row(const uint32_t* v, float alpha, con
 template <int kFmt>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     mx_linear_pair_kernel(const __grid_constant__ MxLinearParams p) {
-  constexpr int ST = kMxStages, KT = mx_stage_tiles(kFmt);
+  constexpr int ST = mx_stages(kFmt), KT = mx_stage_tiles(kFmt);
   constexpr int kSfA = 512 * KT, kSfB = 1024 * KT;  // bytes of a stage's scales
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -207,12 +261,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   __shared__ int abort_flag;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int nk = (p.row_bytes + 127) / 128;
   const int pair = static_cast<int>(blockIdx.x >> 1), n_pairs = static_cast<int>(gridDim.x >> 1);
-  // 256 x 256 tiles of this pair: t = pair + i * n_pairs (column tile fastest)
-  int n_local = p.tiles > pair ? (p.tiles - 1 - pair) / n_pairs + 1 : 0;
+  // units of this pair: pair + i * n_pairs (column tile fastest)
+  int n_local = p.units > pair ? (p.units - 1 - pair) / n_pairs + 1 : 0;
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
@@ -264,12 +318,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     uint32_t wrap = 1;  // parity of the last release of stage s (none in the first round)
     bool ok = true;
     for (int i = 0; i < n_local && ok; ++i) {
-      const int t = pair + i * n_pairs, nt = t % p.n_tiles;
+      const int u = pair + i * n_pairs, piece = u - p.whole;
+      const int t = piece < 0 ? u : p.whole + p.piece_tile[piece], nt = t % p.n_tiles;
+      const int k0 = piece < 0 ? 0 : p.piece_k0[piece], n = piece < 0 ? nk : p.piece_n[piece];
       // this CTA's rows and columns; rows past the matrix are zero fill and not stored
       const int r0 = (t / p.n_tiles) * 256 + 128 * static_cast<int>(rank);
       const int n0 = nt * kMxTileN, rk = static_cast<int>(rank);
       const int own = n0 + (i & 1 ? 64 : 0) + 96 * rk, shared = n0 + (i & 1 ? 0 : 192) + 32 * rk;
-      for (int kc = 0; kc < nk; ++kc) {
+      for (int kc = 0; kc < n; ++kc) {
         if (issued >= ST && !warp_wait_short(&empty[s], wrap, &abort_flag)) {
           ok = false;
           break;
@@ -277,16 +333,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         const uint32_t bar = full0 + static_cast<uint32_t>(s * sizeof(uint64_t));
         if (elements) {
           if (expect) mbar_arrive_expect_tx(&full[s], 2 * mx_stage_bytes(kFmt));
-          tma_load_2d_pair_if(leader, a0 + s * kMxABytes, &p.x_map, bar, 128 * kc, r0);
-          if (kc == 0 || kc == nk - 1) {
-            tma_load_2d_pair_if(leader, b0 + s * kMxBBytes, &p.w96_map, bar, 128 * kc, own);
-            tma_load_2d_pair_if(leader, b0 + s * kMxBBytes + 96 * 128, &p.w32_map, bar, 128 * kc, shared);
+          tma_load_2d_pair_if(leader, a0 + s * kMxABytes, &p.x_map, bar, 128 * (k0 + kc), r0);
+          if (kc == 0 || kc == n - 1) {
+            tma_load_2d_pair_if(leader, b0 + s * kMxBBytes, &p.w96_map, bar, 128 * (k0 + kc), own);
+            tma_load_2d_pair_if(leader, b0 + s * kMxBBytes + 96 * 128, &p.w32_map, bar, 128 * (k0 + kc), shared);
           } else {
-            tma_load_2d_pair_if(leader, b0 + s * kMxBBytes, &p.w_map, bar, 128 * kc, n0 + 128 * rk);
+            tma_load_2d_pair_if(leader, b0 + s * kMxBBytes, &p.w_map, bar, 128 * (k0 + kc), n0 + 128 * rk);
           }
         } else {
-          tma_load_2d_pair_if(leader, sa0 + s * kSfA, &p.xs_map, bar, 64 * KT * kc, r0 >> 7);
-          tma_load_2d_pair_if(leader, sb0 + s * kSfB, &p.ws_map, bar, 64 * KT * kc, n0 >> 7);
+          tma_load_2d_pair_if(leader, sa0 + s * kSfA, &p.xs_map, bar, 64 * KT * (k0 + kc), r0 >> 7);
+          tma_load_2d_pair_if(leader, sb0 + s * kSfB, &p.ws_map, bar, 64 * KT * (k0 + kc), n0 >> 7);
         }
         ++issued;
         if (++s == ST) {
@@ -322,7 +378,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       tc_fence_after();
       const uint32_t tacc = tbase + 192 * a;
       const uint32_t down = 64 * a, dshared = 192 * (a ^ 1);  // first columns of the own and of the shared part
-      for (int kc = 0; kc < nk; ++kc) {
+      const int piece = pair + i * n_pairs - p.whole;
+      const int n = piece < 0 ? nk : p.piece_n[piece];
+      const int last = piece < 0 || p.piece_k0[piece] + n == nk ? last_steps : 4;
+      for (int kc = 0; kc < n; ++kc) {
         if (!warp_wait_short(&full[s], round, &abort_flag)) {
           ok = false;
           break;
@@ -336,7 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           tmem_copy_scales_pair_if(leader, sfb + 8 * j, at(dSB, lsb + 32 * j));
           tmem_copy_scales_pair_if(leader, sfb + 8 * j + 4, at(dSB, lsb + 32 * (KT + j)));
         }
-        const int steps = kc == nk - 1 ? last_steps : 4;
+        const int steps = kc == n - 1 ? last : 4;
         const uint32_t acc = kc != 0 ? 1u : 0u;
         auto mma = [&](int kk, uint32_t d, uint32_t b, uint32_t sf, int N) {
           // scale tile and byte of step kk
@@ -362,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           tc_fence_after();
           return ok;
         };
-        if (kc == nk - 1) {
+        if (kc == n - 1) {
           if (kc == 0 && !shared_read()) break;
           shared();
           umma_pair_commit_both_if(leader, smem_u32(sh_full));
@@ -398,14 +457,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     const uint32_t acce0 = cluster_addr(acc_empty, 0), she0 = cluster_addr(sh_empty, 0);
     const float4* bias = reinterpret_cast<const float4*>(sBias + 64 * (warp - 4));
     float2* bias2 = reinterpret_cast<float2*>(sBias + 64 * (warp - 4));
-    bias2[lane] = make_float2(0.f, 0.f);
+    auto tile = [&](int i) {  // of unit i (past the last: the first's)
+      const int u = i < n_local ? pair + i * n_pairs : pair;
+      return u < p.whole ? u : p.whole + p.piece_tile[u - p.whole];
+    };
+    // the bias of a tile's columns is loaded a tile ahead
+    auto load_bias = [&](int i) {
+      const int c = tile(i) % p.n_tiles * kMxTileN + 64 * e + 2 * lane;
+      if (p.bias == nullptr || c >= p.d_out) return make_float2(0.f, 0.f);  // d_out is a multiple of 8
+      return make_float2(__ldg(p.bias + c), __ldg(p.bias + c + 1));
+    };
+    float2 next = load_bias(0);
     for (int i = 0; i < n_local; ++i) {
-      const int a = i & 1, t = pair + i * n_pairs;
+      const int a = i & 1, t = tile(i), piece = pair + i * n_pairs - p.whole;
       const int nc = (t % p.n_tiles) * kMxTileN + 64 * e;
       const int r = (t / p.n_tiles) * 256 + 128 * static_cast<int>(rank) + 32 * q + lane;
       __syncwarp();  // the last tile's bias has been read
-      if (p.bias != nullptr && nc + 2 * lane < p.d_out)  // d_out is a multiple of 8
-        bias2[lane] = make_float2(__ldg(p.bias + nc + 2 * lane), __ldg(p.bias + nc + 2 * lane + 1));
+      bias2[lane] = next;
+      next = load_bias(i + 1);
       const bool sh = e == (a ? 0 : 3);
       if (!(sh ? warp_wait_short(sh_full, i & 1, &abort_flag) : warp_wait_short(&acc_full[a], (i >> 1) & 1, &abort_flag))) break;
       tc_fence_after();
@@ -416,8 +485,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       tmem_ld_wait32(v + 32);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(sh ? she0 : acce0 + static_cast<uint32_t>(a * sizeof(uint64_t)));
-      if (r < p.M) {
+      if (lane == 0) mbar_arrive_cluster_relaxed(sh ? she0 : acce0 + static_cast<uint32_t>(a * sizeof(uint64_t)));
+      if (piece >= 0) {
+        float* part = p.part + (static_cast<size_t>(piece) * 256 + 128 * rank + 32 * q + lane) * 256 + 64 * e;
+        if (r < p.M) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) st_global32(part + 8 * c, v + 8 * c);
+        }
+      } else if (r < p.M) {
         __nv_bfloat16* y = p.Y + static_cast<size_t>(r) * p.d_out + nc;
         if (p.act == 1) mx_store_row<true>(v, p.alpha, bias, y, p.d_out - nc, p.wide);
         else mx_store_row<false>(v, p.alpha, bias, y, p.d_out - nc, p.wide);
@@ -430,6 +505,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   cluster_sync();  // the partner's MMAs, copies and arrivals are done
   tc_fence_after();
   if (warp == 2) tmem_dealloc_pair(*tmem_slot, 512);
+}
+
+// The tiles that were split: act(alpha sum of the pieces + bias), the pieces added
+// in order. A thread takes 8 columns of a row.
+struct MxMergeParams {
+  const float* part;
+  const float* bias;
+  __nv_bfloat16* Y;
+  float alpha;
+  int M, d_out, act, n_tiles, whole, split;
+};
+__global__ void __launch_bounds__(256) mx_linear_merge_kernel(const MxMergeParams p) {
+  const int tile = blockIdx.x >> 5, t = p.whole + tile;  // 32 CTAs of 8 rows for a tile
+  const int row = (blockIdx.x & 31) * 8 + (threadIdx.x >> 5), col = (threadIdx.x & 31) * 8;
+  const int r = (t / p.n_tiles) * 256 + row, c = (t % p.n_tiles) * kMxTileN + col;
+  if (r >= p.M || c >= p.d_out) return;  // d_out is a multiple of 8
+  const float* part = p.part + (static_cast<size_t>(tile) * p.split * 256 + row) * 256 + col;
+  float f[8] = {};
+  for (int k = 0; k < p.split; ++k) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(part + static_cast<size_t>(k) * 65536));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(part + static_cast<size_t>(k) * 65536) + 1);
+    f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
+    f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = fmaf(f[k], p.alpha, p.bias != nullptr ? __ldg(p.bias + c + k) : 0.f);
+  if (p.act == 1) {
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) gelu_tanh_2(f[k], f[k + 1]);
+  }
+  store8(p.Y + static_cast<size_t>(r) * p.d_out + c, f);
 }
 
 }  // namespace safe

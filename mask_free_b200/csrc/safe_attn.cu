@@ -650,6 +650,7 @@ bool encode_bytes_map(CUtensorMap* map, const void* base, bool words, uint64_t i
 // How many CTA pairs of a kernel can be resident at once on the current device.
 template <auto kKernel>
 int resident_pairs(int threads, int smem) {
+  if (!allow_smem<kKernel>(smem)) return device_sms() / 2;
   static std::mutex mu;
   static int cached[64] = {};
   int dev = 0;
@@ -668,9 +669,48 @@ int resident_pairs(int threads, int smem) {
   return n;
 }
 
+// How a microscaled layer's 256 x 256 tiles go over the resident CTA pairs: whole
+// tiles in full waves, and those of the last, partial wave in pieces along
+// d_in, as many as there are pairs for, whose fp32 sums a second kernel adds.
+// The second launch costs what 12 stages do, the pieces' way through memory 28
+// for 64 full pieces, so a split has to save more. Measured with / without
+// (mxfp8, d_in 9216, d_out 2304): 2458 rows 49 / 57 us (90 tiles on 74 pairs, the
+// last 16 in 4 pieces), 300 rows 27 / 33, 2 rows 18 / 29; where it would not
+// pay: 1000 rows (halves) 35 / 33, nvfp4 (half the stages) 2458 rows 35 / 34.
+struct MxPlan {
+  int pairs, n_tiles, rest, whole, split;
+  int64_t units;
+  size_t part_bytes;
+};
+MxPlan mx_linear_plan(int64_t M, int d_out, int row_bytes, int pairs, bool may_split) {
+  MxPlan p{};
+  p.pairs = pairs;
+  p.n_tiles = (d_out + kMxTileN - 1) / kMxTileN;
+  const int64_t tiles = (M + 255) / 256 * p.n_tiles;
+  const int nk = (row_bytes + 127) / 128, rest = static_cast<int>(tiles % pairs);
+  int split = rest > 0 ? pairs / rest : 1;
+  if (split > nk / 4) split = nk / 4;  // pieces of four stages at least
+  const int64_t row_tiles = (M + 255) / 256, rows = M / row_tiles;  // of a tile, on average
+  const int64_t cost = 12 + 28 * rows * rest * split / (64 * 256);
+  if (!may_split || split < 2 || nk - (nk + split - 1) / split <= cost || tiles > INT_MAX || rest * split > kMxPieces ||
+      nk > 65535)
+    split = 1;
+  p.split = split;
+  p.rest = split > 1 ? rest : 0;
+  p.whole = static_cast<int>(tiles - p.rest);
+  p.units = tiles - p.rest + static_cast<int64_t>(p.rest) * split;
+  p.part_bytes = static_cast<size_t>(p.rest) * split * 256 * 256 * sizeof(float);
+  return p;
+}
+int mx_linear_pairs(int fmt) {
+  if (fmt == SAFE_MXFP8) return resident_pairs<mx_linear_pair_kernel<kMxFp8>>(kMxThreads, mx_linear_smem(kMxFp8));
+  if (fmt == SAFE_MXFP4) return resident_pairs<mx_linear_pair_kernel<kMxFp4>>(kMxThreads, mx_linear_smem(kMxFp4));
+  return resident_pairs<mx_linear_pair_kernel<kNvFp4>>(kMxThreads, mx_linear_smem(kNvFp4));
+}
+
 template <int kFmt>
 safe_status launch_mx_linear(MxLinearParams& p, const void* X, const void* Xs, const void* W, const void* Ws, int d_in,
-                             cudaStream_t s) {
+                             const MxPlan& plan, cudaStream_t s) {
   constexpr int smem = mx_linear_smem(kFmt), words = 64 * mx_stage_tiles(kFmt);
   const uint64_t ct = static_cast<uint64_t>(mx_tiles(d_in, kFmt)) * 64, rb = static_cast<uint64_t>(p.row_bytes);
   if (!encode_bytes_map(&p.x_map, X, false, rb, static_cast<uint64_t>(p.M), 128, 128) ||
@@ -680,14 +720,14 @@ safe_status launch_mx_linear(MxLinearParams& p, const void* X, const void* Xs, c
       !encode_bytes_map(&p.xs_map, Xs, true, ct, static_cast<uint64_t>((p.M + 127LL) / 128), words, 1) ||
       !encode_bytes_map(&p.ws_map, Ws, true, ct, static_cast<uint64_t>((p.d_out + 127) / 128), words, 2))
     return SAFE_ERR_CUDA;
-  p.n_tiles = (p.d_out + kMxTileN - 1) / kMxTileN;
-  const int64_t tiles = (static_cast<int64_t>(p.M) + 255) / 256 * p.n_tiles;
-  if (tiles > INT_MAX) return SAFE_ERR_UNSUPPORTED;
-  p.tiles = static_cast<int>(tiles);
   if (!allow_smem<mx_linear_pair_kernel<kFmt>>(smem)) return SAFE_ERR_CUDA;
-  const int mp = resident_pairs<mx_linear_pair_kernel<kFmt>>(kMxThreads, smem);
-  const int pairs = static_cast<int>(tiles < mp ? tiles : mp);
+  const int pairs = p.units < plan.pairs ? p.units : plan.pairs;
   mx_linear_pair_kernel<kFmt><<<2 * pairs, kMxThreads, smem, s>>>(p);
+  if (launch_status() != SAFE_OK) return SAFE_ERR_CUDA;
+  if (plan.rest > 0) {
+    MxMergeParams m{p.part, p.bias, p.Y, p.alpha, p.M, p.d_out, p.act, p.n_tiles, p.whole, plan.split};
+    mx_linear_merge_kernel<<<32 * plan.rest, 256, 0, s>>>(m);
+  }
   return launch_status();
 }
 
@@ -1152,9 +1192,8 @@ safe_status safe_rope(const void* q, const int64_t q_strides[3], void* oq, const
                       void* stream) {
   const size_t e = float_size(dtype);
   if (e == 0) return SAFE_ERR_UNSUPPORTED;
-  if (q == nullptr || oq == nullptr || q_strides == nullptr || oq_strides == nullptr || Hq < 1) return SAFE_ERR_INVALID_ARG;
-  if (k == nullptr ? (ok != nullptr || Hk != 0) : (ok == nullptr || k_strides == nullptr || ok_strides == nullptr || Hk < 1))
-    return SAFE_ERR_INVALID_ARG;
+  if (q == nullptr || oq == nullptr || Hq < 1) return SAFE_ERR_INVALID_ARG;
+  if (k == nullptr ? (ok != nullptr || Hk != 0) : (ok == nullptr || Hk < 1)) return SAFE_ERR_INVALID_ARG;
   if (!sizes_ok(B, N, Hq) || Hk > 65535 || R < 1 || R > N || (S == nullptr && R != N)) return SAFE_ERR_INVALID_ARG;
   if (d < 2 || r < 2 || r > d || r % 2 != 0 || freq == nullptr || sections == nullptr || !std::isfinite(m))
     return SAFE_ERR_INVALID_ARG;
@@ -1171,7 +1210,10 @@ safe_status safe_rope(const void* q, const int64_t q_strides[3], void* oq, const
   bool vec = d % 8 == 0 && r % 16 == 0;
   const void* xs[2] = {q, k};
   void* os[2] = {oq, ok};
-  const int64_t* st[4] = {q_strides, oq_strides, k_strides, ok_strides};
+  const int64_t q_own[3] = {static_cast<int64_t>(R) * Hq * d, static_cast<int64_t>(Hq) * d, d};
+  const int64_t k_own[3] = {static_cast<int64_t>(R) * Hk * d, static_cast<int64_t>(Hk) * d, d};
+  const int64_t* st[4] = {q_strides ? q_strides : q_own, oq_strides ? oq_strides : q_own, k_strides ? k_strides : k_own,
+                          ok_strides ? ok_strides : k_own};
   const int heads[2] = {Hq, Hk}, n = k != nullptr ? 2 : 1;
   View4 in[2], out[2];
   bool in_place[2] = {};
@@ -1277,9 +1319,16 @@ safe_status safe_mx_dequantize(const void* data, const void* scales, int fmt, fl
   }
 }
 
+size_t safe_mx_linear_workspace_bytes(int64_t rows, int d_in, int d_out, int fmt) {
+  if (fmt < SAFE_MXFP8 || fmt > SAFE_NVFP4 || rows < 1 || rows > INT_MAX || d_in < 64 || d_in % 32 != 0 || d_out < 8 ||
+      d_out % 8 != 0)
+    return 0;
+  return mx_linear_plan(rows, d_out, fmt == SAFE_MXFP8 ? d_in : d_in / 2, mx_linear_pairs(fmt), true).part_bytes;
+}
+
 safe_status safe_mx_linear(const void* X, const void* X_scales, const void* Wt, const void* Wt_scales, int fmt,
                            float alpha, const float* bias, int act, void* Y, int64_t rows, int d_in, int d_out,
-                           void* stream) {
+                           void* ws, size_t ws_bytes, void* stream) {
   if (!aligned16(X) || !aligned16(X_scales) || !aligned16(Wt) || !aligned16(Wt_scales) || !aligned16(Y) ||
       !aligned_to(bias, 4))
     return SAFE_ERR_INVALID_ARG;
@@ -1292,7 +1341,33 @@ safe_status safe_mx_linear(const void* X, const void* X_scales, const void* Wt, 
       overlap(Y, yb, Wt, static_cast<size_t>(d_out) * row_bytes) ||
       overlap(Y, yb, Wt_scales, safe_mx_scale_bytes(d_out, d_in, fmt)))
     return SAFE_ERR_INVALID_ARG;
+  const int pairs = mx_linear_pairs(fmt);
+  MxPlan plan = mx_linear_plan(rows, d_out, row_bytes, pairs, ws != nullptr);
+  if (plan.part_bytes > 0) {
+    if (ws_bytes < plan.part_bytes) {
+      plan = mx_linear_plan(rows, d_out, row_bytes, pairs, false);
+    } else if (!aligned_to(ws, 32) || overlap(ws, plan.part_bytes, Y, yb) ||
+               overlap(ws, plan.part_bytes, X, static_cast<size_t>(rows) * row_bytes) ||
+               overlap(ws, plan.part_bytes, X_scales, safe_mx_scale_bytes(rows, d_in, fmt)) ||
+               overlap(ws, plan.part_bytes, Wt, static_cast<size_t>(d_out) * row_bytes) ||
+               overlap(ws, plan.part_bytes, Wt_scales, safe_mx_scale_bytes(d_out, d_in, fmt)) ||
+               overlap(ws, plan.part_bytes, bias, static_cast<size_t>(d_out) * 4)) {
+      return SAFE_ERR_INVALID_ARG;
+    }
+  }
+  if (plan.units > INT_MAX) return SAFE_ERR_UNSUPPORTED;
   MxLinearParams p{};
+  p.n_tiles = plan.n_tiles;
+  p.whole = plan.whole;
+  for (int t = 0; t < plan.rest; ++t)
+    for (int k = 0, nk = (row_bytes + 127) / 128; k < plan.split; ++k) {
+      const int i = t * plan.split + k, k0 = nk * k / plan.split;
+      p.piece_tile[i] = static_cast<uint16_t>(t);
+      p.piece_k0[i] = static_cast<uint16_t>(k0);
+      p.piece_n[i] = static_cast<uint16_t>(nk * (k + 1) / plan.split - k0);
+    }
+  p.units = static_cast<int>(plan.units);
+  p.part = static_cast<float*>(ws);
   p.bias = bias;
   p.Y = static_cast<__nv_bfloat16*>(Y);
   p.wide = d_out % 16 == 0 && aligned_to(Y, 32);
@@ -1302,9 +1377,9 @@ safe_status safe_mx_linear(const void* X, const void* X_scales, const void* Wt, 
   p.d_out = d_out;
   p.act = act;
   switch (fmt) {
-    case SAFE_MXFP8: return launch_mx_linear<kMxFp8>(p, X, X_scales, Wt, Wt_scales, d_in, as_stream(stream));
-    case SAFE_MXFP4: return launch_mx_linear<kMxFp4>(p, X, X_scales, Wt, Wt_scales, d_in, as_stream(stream));
-    default: return launch_mx_linear<kNvFp4>(p, X, X_scales, Wt, Wt_scales, d_in, as_stream(stream));
+    case SAFE_MXFP8: return launch_mx_linear<kMxFp8>(p, X, X_scales, Wt, Wt_scales, d_in, plan, as_stream(stream));
+    case SAFE_MXFP4: return launch_mx_linear<kMxFp4>(p, X, X_scales, Wt, Wt_scales, d_in, plan, as_stream(stream));
+    default: return launch_mx_linear<kNvFp4>(p, X, X_scales, Wt, Wt_scales, d_in, plan, as_stream(stream));
   }
 }
 

@@ -59,11 +59,13 @@ _SIGS = {
     "safe_mx_scale_bytes": [_i64, _i, _i],
     "safe_mx_quantize": [_vp, _i, _vp, _i, _i, _f, _vp, _vp, _i, _i, _i, _vp],
     "safe_mx_dequantize": [_vp, _vp, _i, _f, _vp, _i, _i64, _i, _vp],
-    "safe_mx_linear": [_vp, _vp, _vp, _vp, _i, _f, _vp, _i, _vp, _i64, _i, _i, _vp],
+    "safe_mx_linear_workspace_bytes": [_i64, _i, _i, _i],
+    "safe_mx_linear": [_vp, _vp, _vp, _vp, _i, _f, _vp, _i, _vp, _i64, _i, _i, _vp, _sz, _vp],
 }
 _RESTYPES = {"safe_pcsp_workspace_bytes": _sz, "safe_attn_workspace_bytes": _sz, "safe_sensitivity_workspace_bytes": _sz,
              "safe_gather_linear_workspace_bytes": _sz, "safe_srsu_workspace_bytes": _sz,
-             "safe_mx_scale_bytes": _sz, "safe_status_string": ctypes.c_char_p}
+             "safe_mx_scale_bytes": _sz,
+             "safe_mx_linear_workspace_bytes": _sz, "safe_status_string": ctypes.c_char_p}
 
 
 class SafeError(RuntimeError):
@@ -521,17 +523,18 @@ _FORMATS = {"mxfp8": 0, "mxfp4": 1, "nvfp4": 2}
 _i64x3 = ctypes.c_int64 * 3
 
 
+def _on(dev: torch.device, fn, *args):
+    """fn(*args) with `dev` as the current device."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(dev.index):
+        return fn(*args)
+
+
 def _run(name: str, dev: torch.device, *args):
     """Call entry point `name` on `dev` (which need not be the current device)
     with that device's current stream as the last argument."""
-    fn, idx = getattr(lib(), name), dev.index
-    if idx is None:
-        st = fn(*args, _stream())
-    elif idx == torch.cuda.current_device():
-        st = fn(*args, _raw_stream(idx))
-    else:
-        with torch.cuda.device(idx):
-            st = fn(*args, _raw_stream(idx))
+    st = _on(dev, getattr(lib(), name), *args, _stream() if dev.index is None else _raw_stream(dev.index))
     if st != SAFE_OK:
         raise SafeError(name, st)
 
@@ -788,6 +791,8 @@ def _heads(t, name: str, dtype, B, R, d, dev):
     shape = t.shape
     if t.dtype is not dtype or len(shape) != 4 or shape[0] != B or shape[1] != R or shape[2] < 1 or shape[3] != d:
         raise ValueError(f"{name} must be {dtype} of shape ({B}, {R}, heads, {d}), got {t.dtype} {tuple(shape)}")
+    if t.is_contiguous():
+        return shape[2], None
     b, n, h, one = t.stride()
     if one != 1:
         raise ValueError(f"{name} must be contiguous in its last dim")
@@ -849,10 +854,9 @@ def rope(q, k, table: RopeTable, pos=None, S=None, interleaved=False, inplace=Fa
         oq, ok, oqs, oks = q, k, qs, ks
     else:
         oq, ok = (None, None) if out is None else out
-        oks = None
+        oqs = oks = None
         if oq is None:
             oq = _out_like(None, "", q, dtype, q.shape)
-            oqs = _i64x3(R * H * d, H * d, d)
         else:
             n, oqs = _heads(oq, "out[0]", dtype, B, R, d, dev)
             if n != H:
@@ -862,7 +866,6 @@ def rope(q, k, table: RopeTable, pos=None, S=None, interleaved=False, inplace=Fa
                 raise ValueError("out[1] needs k")
         elif ok is None:
             ok = _out_like(None, "", k, dtype, k.shape)
-            oks = _i64x3(R * Hk * d, Hk * d, d)
         else:
             n, oks = _heads(ok, "out[1]", dtype, B, R, d, dev)
             if n != Hk:
@@ -926,11 +929,19 @@ def mx_dequantize(m: MxTensor, dtype=torch.bfloat16, out=None):
     return out
 
 
-def mx_linear(X: MxTensor, W: MxTensor, bias=None, act="none", out=None):
+def mx_linear_workspace_bytes(rows: int, d_in: int, d_out: int, fmt: str) -> int:
+    if fmt not in _FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(_FORMATS)}, got {fmt!r}")
+    return int(lib().safe_mx_linear_workspace_bytes(rows, d_in, d_out, _FORMATS[fmt]))
+
+
+def mx_linear(X: MxTensor, W: MxTensor, bias=None, act="none", out=None, ws=None):
     """A row-wise layer with microscaled operands, Y = act(X W^T + bias): X
     [..., d_in] (mx_quantize, rms_norm with quant; the rows of S for the
     row-selective block), W [d_out, d_in], both of one format; bias [d_out]
-    fp32, act "none" or "gelu_tanh". Returns bf16 [..., d_out]."""
+    fp32, act "none" or "gelu_tanh". Returns bf16 [..., d_out].
+    ws: the workspace for splitting the last wave's tiles along d_in (a fresh
+    one when None; False: every tile whole)."""
     if not isinstance(X, MxTensor) or not isinstance(W, MxTensor):
         raise ValueError("X and W must be MxTensors")
     if X.fmt != W.fmt:
@@ -948,6 +959,15 @@ def mx_linear(X: MxTensor, W: MxTensor, bias=None, act="none", out=None):
     if not 2.0 ** -126 <= abs(alpha) < 2.0 ** 128:
         raise ValueError(f"the product of the operands' factors is out of range: {alpha}")
     out = _out_like(out, "out", X.scales, torch.bfloat16, (*X.data.shape[:-1], d_out))
-    _run("safe_mx_linear", dev, X.data.data_ptr(), X.scales.data_ptr(), W.data.data_ptr(), W.scales.data_ptr(),
-         _FORMATS[X.fmt], alpha, _ptr(bias), _ACTS[act], out.data_ptr(), rows, d_in, d_out)
+    code, wp, wb = _FORMATS[X.fmt], None, 0
+    if ws is None:
+        wb = _on(dev, lib().safe_mx_linear_workspace_bytes, rows, d_in, d_out, code)
+        if wb:
+            ws = X.scales.new_empty(wb)
+            wp = ws.data_ptr()
+    elif ws is not False:
+        _need(ws, "ws", torch.uint8, 1, device=dev)
+        wp, wb = ws.data_ptr(), ws.numel()
+    _run("safe_mx_linear", dev, X.data.data_ptr(), X.scales.data_ptr(), W.data.data_ptr(), W.scales.data_ptr(), code,
+         alpha, _ptr(bias), _ACTS[act], out.data_ptr(), rows, d_in, d_out, wp, wb)
     return out

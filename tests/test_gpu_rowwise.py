@@ -504,6 +504,33 @@ def test_mx_linear_many_tiles_and_nan_rows(fmt):
     assert torch.equal(bad[rest], y[rest]) and ops.device_status() == 0
 
 
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,d_in,d_out,act", [(1, 9216, 264, "none"), (300, 9216, 520, "gelu_tanh"),
+                                              (2458, 9216, 2304, "none"), (700, 20000, 1000, "gelu_tanh")])
+def test_mx_linear_split_along_d_in(fmt, M, d_in, d_out, act):
+    # the last wave's tiles in pieces: against the oracle on some rows, and
+    # against whole tiles, which add in another order
+    gx, gw = (0.03, 0.2) if fmt == "nvfp4" else (1.0, 1.0)
+    X, mX = operand(M, d_in, fmt, 7, gx)
+    W, mW = operand(d_out, d_in, fmt, 8, gw)
+    pick = np.unique(np.r_[0, M - 1, np.random.default_rng(1).choice(M, min(M, 60), replace=False)])
+    bias = np.random.default_rng(3).normal(size=d_out).astype(np.float32) * float(np.abs(X[pick] @ W[:8].T).mean())
+    n = ops.mx_linear_workspace_bytes(M, d_in, d_out, fmt)
+    assert (n > 0) == (M != 2458 or fmt == "mxfp8")  # 36 stages of 4 bits: not worth it
+    buf, ws = guarded((n,), torch.uint8)
+    obuf, out = guarded((M, d_out), bf16)
+    y = ops.mx_linear(mX, mW, dev(bias), act, out=out, ws=ws)
+    at = torch.from_numpy(pick).to(DEV)
+    linear_check(y[at], X[pick], W, bias, act)
+    assert untouched(buf) and untouched(obuf)
+    assert torch.equal(ops.mx_linear(mX, mW, dev(bias), act), y)
+    whole = ops.mx_linear(mX, mW, dev(bias), act, ws=False)
+    linear_check(whole[at], X[pick], W, bias, act)
+    # a workspace that is too small: whole tiles
+    assert torch.equal(ops.mx_linear(mX, mW, dev(bias), act, ws=ws[:max(n - 32, 0)]), whole)
+    assert ops.device_status() == 0
+
+
 def test_mx_linear_gelu_over_its_range():
     X, mX = operand(20, 64, "mxfp8", 1)
     W, mW = operand(512, 64, "mxfp8", 2)
@@ -511,6 +538,11 @@ def test_mx_linear_gelu_over_its_range():
     zero = ops.MxTensor(torch.zeros_like(mX.data.view(torch.uint8)).view(torch.float8_e4m3fn), mX.scales, "mxfp8")
     bias = np.linspace(-12, 12, 512).astype(np.float32)
     linear_check(ops.mx_linear(zero, mW, dev(bias), "gelu_tanh"), X, W, bias, "gelu_tanh")
+    # far values: x or (nearly) nothing, a NaN stays a NaN beside them
+    far = np.array([1e4, -1e4, 1e20, -1e20, np.inf, -np.inf, np.nan, 1.0] * 64, dtype=np.float32)
+    y = to64(ops.mx_linear(zero, mW, dev(far), "gelu_tanh"))[:, :8]
+    assert np.allclose(y[:, [0, 2, 7]], [1e4, 1e20, 0.8411920], rtol=2.0 ** -8) and np.all(y[:, 4] == np.inf)
+    assert np.all(np.abs(y[:, [1, 3, 5]]) < 1e-16) and np.all(np.isnan(y[:, 6]))
 
 
 # ---------------------------------------------------------------- together

@@ -145,7 +145,7 @@ def test_valid_calls_reach_the_abi_with_their_sizes(rec):
     oq, ok = ops.rope(q, kk, tab)
     a = _last(rec, "safe_rope")
     assert oq.shape == q.shape and ok.shape == kk.shape and a[4] == 6 and a[9] == 2 and a[10] == 3
-    assert list(a[1]) == [N * 384, 384, 64] and a[17:22] == (B, N, N, 64, 32)
+    assert a[17:22] == (B, N, N, 64, 32)
     qkv = t(B, k, 10, 64)
     oq, ok = ops.rope(qkv[:, :, :6], qkv[:, :, 6:8], table(64, [16, 16]), pos=t(N, 2, dtype=i32), S=S, inplace=True)
     a = _last(rec, "safe_rope")
@@ -225,6 +225,7 @@ def test_mismatched_arguments_are_refused_before_any_launch(rec):
     _refused(ops.mx_linear, mx(B, N), mx(40), bias=t(41, dtype=f32))
     _refused(ops.mx_linear, mx(B, N), mx(40), act="relu")
     _refused(ops.mx_linear, mx(B, N), mx(40), out=t(B, N, 41))
+    _refused(ops.mx_linear, mx(B, N), mx(40), ws=t(64))
     _refused(ops.mx_linear, mx(B, N, fmt="nvfp4", scale=2.0 ** -80), mx(40, fmt="nvfp4", scale=2.0 ** -80))
     _refused(ops.MxTensor, torch.zeros((4, 64), dtype=u8), torch.zeros(512, dtype=u8), "mxfp8")
     _refused(ops.MxTensor, torch.zeros((4, 64), dtype=u8), torch.zeros(512, dtype=u8), "nvfp4")  # two tiles along a row
@@ -325,10 +326,20 @@ def test_microscaled_entry_points_validate_on_host(lib):
     assert deq(data=None) == 1 and deq(sc=None) == 1 and deq(Y=None) == 1 and deq(dtype=1) == 2 and deq(rows=0) == 1
     assert deq(D=40) == 1 and deq(g=2.0) == 1 and deq(Y=at(0)) == 1 and deq(Y=at(1)) == 1 and deq(rows=2 ** 31) == 1
 
-    def lin(X=at(0), Xs=at(1), W=at(2), Ws=at(3), fmt=2, a=1.0, bias=None, act=0, Y=at(4), rows=16, i=64, o=64):
-        return lib.safe_mx_linear(X, Xs, W, Ws, fmt, a, bias, act, Y, rows, i, o, None)
+    def lin(X=at(0), Xs=at(1), W=at(2), Ws=at(3), fmt=2, a=1.0, bias=None, act=0, Y=at(4), rows=16, i=64, o=64, ws=None, wb=0):
+        return lib.safe_mx_linear(X, Xs, W, Ws, fmt, a, bias, act, Y, rows, i, o, ws, wb, None)
 
     assert lin(X=None) == 1 and lin(Xs=None) == 1 and lin(W=None) == 1 and lin(Ws=None) == 1 and lin(Y=None) == 1
     assert lin(fmt=3) == 1 and lin(a=float("nan")) == 1 and lin(a=0.0) == 1 and lin(act=2) == 1
     assert lin(rows=0) == 1 and lin(rows=2 ** 31) == 1 and lin(i=32) == 1 and lin(i=80) == 1 and lin(o=12) == 1 and lin(o=0) == 1
     assert lin(bias=ctypes.c_void_p(0x100002)) == 1 and lin(Y=at(0)) == 1 and lin(Y=at(3)) == 1
+    # the split of the last wave's tiles (9 of 74 pairs, 72 stages): its workspace, apart from the rest
+    big = dict(fmt=0, rows=200, i=9216, o=2304)
+    n = lib.safe_mx_linear_workspace_bytes(200, 9216, 2304, 0)
+    assert n == 9 * 8 * 256 * 256 * 4
+    assert lin(**big, ws=ctypes.c_void_p(0x10000010), wb=n) == 1 and lin(**big, ws=at(4), wb=n) == 1
+    assert lin(**big, ws=at(2), wb=n) == 1
+    assert lib.safe_mx_linear_workspace_bytes(200, 2304, 2304, 2) == 0     # 9 stages: not worth it
+    assert lib.safe_mx_linear_workspace_bytes(18944, 9216, 2304, 0) == 0   # whole waves
+    assert lib.safe_mx_linear_workspace_bytes(0, 64, 64, 0) == 0 and lib.safe_mx_linear_workspace_bytes(4, 80, 64, 0) == 0
+    assert lib.safe_mx_linear_workspace_bytes(4, 64, 12, 0) == 0 and lib.safe_mx_linear_workspace_bytes(4, 64, 64, 3) == 0
