@@ -53,7 +53,7 @@ __device__ __forceinline__ bool norm_rows(const NormParams& p, long long row, bo
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* part) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = TPR < 32 ? TPR / 2 : 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (TPR > 32) {
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
@@ -64,59 +64,46 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
-// TPR threads take a row, each NV units of VEC consecutive elements, and keep
-// it in registers between the sum and the output: one read of x and res.
-// VEC = 8 where rows and tensors are 16-byte aligned, else 1.
-template <typename T, int VEC, int NV, int TPR>
+// How the elements of a row are accessed:
+//   kNormVec    8 at a time; rows and tensors 16-byte aligned (D a multiple of 8)
+//   kNormShift  8 at a time from the aligned address at or before the row's
+//               first element, for any D, where every tensor has its row at
+//               the same place (no S) and begins 16-byte aligned; elements of
+//               the neighbouring rows are masked, edges stored one by one
+//   kNormOne    one by one
+// Measured (bf16 with the residual, 51200 rows): D = 2304 143 us (6.6 TB/s),
+// 2303 190 us shifted, 472 one by one.
+enum : int { kNormVec, kNormShift, kNormOne };
+
+// TPR threads take a row, each NV units of 8 elements (one in kNormOne), and keep
+// it in registers between the sum and the output: one read of x and res. Bound
+// by memory. Few registers for each thread and many rows at once keep more
+// loads in flight than long rows in one warp: D = 2304 on 128 threads with 3
+// units each takes 47 us for 12800 rows (8-bit output), on a warp with 10
+// units 53.
+template <typename T, int kMode, int NV, int TPR>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const NormParams p) {
-  constexpr int kRowsCta = TPR < 128 ? 128 / TPR : 1;
-  __shared__ float part[TPR / 32];
+  constexpr int kRowsCta = TPR < 128 ? 128 / TPR : 1, VEC = kMode == kNormOne ? 1 : 8;
+  __shared__ float part[TPR < 32 ? 1 : TPR / 32];
   const int t = threadIdx.x % TPR;
   const long long row = static_cast<long long>(blockIdx.x) * kRowsCta + threadIdx.x / TPR;
-  if (row >= p.rows_pad) return;  // whole rows leave: whole warps, or the CTA
-  const int units = p.D / VEC;
-  if (row >= p.rows) {  // fills the last scale tile up
-    for (int j = 4 * t; j < 4 * p.ct; j += 4 * TPR)
-      *reinterpret_cast<uint32_t*>(p.q_scales + mx_scale_at(row, j, p.ct)) = 0u;
-    return;
-  }
-  long long xr, rr, hr;
-  const bool ok = norm_rows(p, row, t == 0, xr, rr, hr);
+  // rows past the last take part in the shuffles as zeros; those that fill the
+  // last scale tile up write their scales, zeros too
+  const bool live = row < p.rows;
+  long long xr = 0, rr = 0, hr = 0;
+  const bool ok = live && norm_rows(p, row, t == 0, xr, rr, hr);
   const T* x = static_cast<const T*>(p.x) + (ok ? xr : 0) * p.D;
   const T* res = p.res != nullptr ? static_cast<const T*>(p.res) + (ok ? rr : 0) * p.D : nullptr;
-  T* h = p.h != nullptr ? static_cast<T*>(p.h) + (ok ? hr : p.h_full ? 0 : row) * p.D : nullptr;
-  const bool h_write = p.h != nullptr && (ok || !p.h_full);
+  T* h = p.h != nullptr ? static_cast<T*>(p.h) + (ok ? hr : p.h_full || !live ? 0 : row) * p.D : nullptr;
+  T* y = p.y != nullptr ? static_cast<T*>(p.y) + (live ? row : 0) * p.D : nullptr;
+  const bool h_write = p.h != nullptr && (ok || (live && !p.h_full));
+  // first element of unit u (shifted: of the row's first whole unit or before), units
+  const int shift = kMode == kNormShift ? static_cast<int>((row * p.D) & 7) : 0;
+  const int units = kMode == kNormOne ? p.D : (p.D + shift + 7) / 8;
+  const long long left = kMode == kNormShift ? (p.rows - row) * p.D : 0;  // elements of the tensor from the row's first on
 
   float v[NV * VEC];
-  if constexpr (VEC == 8) {
-    Raw8<T> a[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int u = i * TPR + t;
-      a[i].zero();
-      if (ok && u < units) a[i].load(x + u * 8);
-    }
-    if (res != nullptr) {
-      Raw8<T> b[NV];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int u = i * TPR + t;
-        b[i].zero();
-        if (ok && u < units) b[i].load(res + u * 8);
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float f[8];
-        a[i].get(v + 8 * i);
-        b[i].get(f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[8 * i + e] += f[e];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) a[i].get(v + 8 * i);
-    }
-  } else {
+  if constexpr (kMode == kNormOne) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int u = i * TPR + t;
@@ -129,6 +116,46 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const N
         if (ok && u < units) v[i] += to_float(res[u]);
       }
     }
+  } else {
+    auto load = [&](Raw8<T>& r, const T* f, int u) {
+      r.zero();
+      if (!ok || u >= units) return;
+      if (kMode == kNormVec || 8 * u - shift + 8 <= left) {
+        r.load(f + (8 * u - shift));
+      } else {  // the tensor ends inside this unit
+        T* e = reinterpret_cast<T*>(&r);
+        for (int k = 0; k < 8; ++k)
+          if (8 * u - shift + k >= 0 && 8 * u - shift + k < p.D) e[k] = f[8 * u - shift + k];
+      }
+    };
+    Raw8<T> a[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) load(a[i], x, i * TPR + t);
+    if (res != nullptr) {
+      Raw8<T> b[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) load(b[i], res, i * TPR + t);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float f[8];
+        a[i].get(v + 8 * i);
+        b[i].get(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[8 * i + e] += f[e];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) a[i].get(v + 8 * i);
+    }
+    if constexpr (kMode == kNormShift) {  // the neighbouring rows' elements
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int at = 8 * (i * TPR + t) - shift + e;
+          if (at < 0 || at >= p.D) v[8 * i + e] = 0.f;
+        }
+    }
   }
   float ss = 0.f;
 #pragma unroll
@@ -136,53 +163,71 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const N
   ss = row_sum<TPR>(ss, part);
   const float rstd = ok ? 1.f / sqrtf(ss / static_cast<float>(p.D) + p.eps) : 0.f;
 
-  T* y = p.y != nullptr ? static_cast<T*>(p.y) + row * p.D : nullptr;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int u = i * TPR + t;
     const bool in = u < units;
-    if constexpr (VEC == 8) {
-      if (in && h_write) store8(h + u * 8, v + 8 * i);
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = v[8 * i + e] * rstd;
-      if (in && p.w != nullptr) {
-        const float4 w0 = __ldg(reinterpret_cast<const float4*>(p.w) + 2 * u);
-        const float4 w1 = __ldg(reinterpret_cast<const float4*>(p.w) + 2 * u + 1);
-        f[0] *= w0.x; f[1] *= w0.y; f[2] *= w0.z; f[3] *= w0.w;
-        f[4] *= w1.x; f[5] *= w1.y; f[6] *= w1.z; f[7] *= w1.w;
-      }
-      if (!ok) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = 0.f;
-      }
-      if (in && y != nullptr) store8(y + u * 8, f);
-      if (p.q != nullptr) {
-        // blocks of 32: four threads; a word of scales: sixteen (D is a
-        // multiple of 32, so a block is inside the row or past its end)
-        uint32_t amax = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(f[e]) & 0x7fffffffu);
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        float inv;
-        uint32_t word = e8m0_scale<8>(amax, inv);
-        if (!in) word = 0;
-        word <<= 8 * ((t >> 2) & 3);
-        word |= __shfl_xor_sync(0xffffffffu, word, 4);
-        word |= __shfl_xor_sync(0xffffffffu, word, 8);
-        if (in) {
-          *reinterpret_cast<uint2*>(p.q + row * p.D + u * 8) =
-              make_uint2(e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                         e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
-          if ((t & 15) == 0) *reinterpret_cast<uint32_t*>(p.q_scales + mx_scale_at(row, u >> 2, p.ct)) = word;
-        }
-      }
-    } else {
+    if constexpr (kMode == kNormOne) {
       if (in) {
         if (h_write) h[u] = from_float<T>(v[i]);
         const float f = ok ? (p.w != nullptr ? v[i] * rstd * __ldg(p.w + u) : v[i] * rstd) : 0.f;
-        if (y != nullptr) y[u] = from_float<T>(f);
+        if (y != nullptr && live) y[u] = from_float<T>(f);
+      }
+      continue;
+    } else {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = v[8 * i + e] * rstd;
+      const int at = 8 * u - shift;  // the unit's first element
+      if (kMode == kNormVec || (at >= 0 && at + 8 <= p.D)) {
+        if (in && h_write) store8(h + at, v + 8 * i);
+        if (in && p.w != nullptr) {
+          if constexpr (kMode == kNormVec) {
+            const float4 w0 = __ldg(reinterpret_cast<const float4*>(p.w) + 2 * u);
+            const float4 w1 = __ldg(reinterpret_cast<const float4*>(p.w) + 2 * u + 1);
+            f[0] *= w0.x; f[1] *= w0.y; f[2] *= w0.z; f[3] *= w0.w;
+            f[4] *= w1.x; f[5] *= w1.y; f[6] *= w1.z; f[7] *= w1.w;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] *= __ldg(p.w + at + e);
+          }
+        }
+        if (!ok) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = 0.f;
+        }
+        if (in && live && y != nullptr) store8(y + at, f);
+      } else if (in && live) {  // an edge of the row
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (at + e >= 0 && at + e < p.D) {
+            if (h_write) h[at + e] = from_float<T>(v[8 * i + e]);
+            if (y != nullptr) y[at + e] = from_float<T>(ok ? (p.w != nullptr ? f[e] * __ldg(p.w + at + e) : f[e]) : 0.f);
+          }
+      }
+      if constexpr (kMode == kNormVec && TPR >= 16) {
+        if (p.q != nullptr) {
+          // blocks of 32: four threads; a word of scales: sixteen (D is a
+          // multiple of 32, so a block is inside the row or past its end)
+          uint32_t amax = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(f[e]) & 0x7fffffffu);
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          float inv;
+          uint32_t word = e8m0_scale<8>(amax, inv);
+          if (!in) word = 0;
+          word <<= 8 * ((t >> 2) & 3);
+          word |= __shfl_xor_sync(0xffffffffu, word, 4);
+          word |= __shfl_xor_sync(0xffffffffu, word, 8);
+          if (in && row < p.rows_pad) {
+            if (live)
+              *reinterpret_cast<uint2*>(p.q + row * p.D + u * 8) =
+                  make_uint2(e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                             e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+            if ((t & 15) == 0) *reinterpret_cast<uint32_t*>(p.q_scales + mx_scale_at(row, u >> 2, p.ct)) = word;
+          }
+        }
       }
     }
   }

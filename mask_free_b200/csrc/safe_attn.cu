@@ -509,39 +509,42 @@ bool allow_smem(int bytes) {
 
 constexpr int kNormMaxVec = 512 * 8 * 10;  // longest row that rms_norm_kernel holds in registers
 
-template <typename T, int VEC, int NV, int TPR>
-void norm_launch(const NormParams& p, cudaStream_t s) {
+template <typename T, int kMode, int NV, int TPR>
+safe_status norm_launch(const NormParams& p, cudaStream_t s) {
   constexpr int rows_cta = TPR < 128 ? 128 / TPR : 1;
-  rms_norm_kernel<T, VEC, NV, TPR>
+  rms_norm_kernel<T, kMode, NV, TPR>
       <<<static_cast<unsigned>((p.rows_pad + rows_cta - 1) / rows_cta), TPR < 128 ? 128 : TPR, 0, s>>>(p);
+  return launch_status();
 }
 
-// The fewest threads whose registers hold a row (a warp for each row needs no
-// barrier), then the smallest number of units for each.
+// The fewest threads that hold a row in a few units each: part of a warp for
+// short rows (51200 rows of 128: 14 us, with a warp for each 25), a warp, 128 threads, 512.
+template <typename T, int kMode>
+safe_status launch_norm_units(const NormParams& p, int units, cudaStream_t s) {
+  if (kMode == kNormVec && units <= 8 && p.q == nullptr) return norm_launch<T, kNormVec, 2, 4>(p, s);
+  if (units <= 32) return norm_launch<T, kMode, 2, 16>(p, s);
+  if (units <= 64) return norm_launch<T, kMode, 2, 32>(p, s);
+  if (units <= 128) return norm_launch<T, kMode, 4, 32>(p, s);
+  if (units <= 256) return norm_launch<T, kMode, 2, 128>(p, s);
+  if (units <= 384) return norm_launch<T, kMode, 3, 128>(p, s);
+  if (units <= 512) return norm_launch<T, kMode, 4, 128>(p, s);
+  if (units <= 896) return norm_launch<T, kMode, 7, 128>(p, s);
+  if (units <= 1280) return norm_launch<T, kMode, 10, 128>(p, s);
+  if (kMode == kNormShift || units <= 2560) return norm_launch<T, kMode, 5, 512>(p, s);
+  return norm_launch<T, kNormVec, 10, 512>(p, s);
+}
+
 template <typename T>
-safe_status launch_norm(const NormParams& p, bool vec, cudaStream_t s) {
+safe_status launch_norm(const NormParams& p, int mode, cudaStream_t s) {
   if (p.rows_pad > INT_MAX) return SAFE_ERR_UNSUPPORTED;
-  if (vec && p.D <= kNormMaxVec) {
-    const int units = p.D / 8;
-    if (units <= 32 * 2) norm_launch<T, 8, 2, 32>(p, s);
-    else if (units <= 32 * 4) norm_launch<T, 8, 4, 32>(p, s);
-    else if (units <= 32 * 6) norm_launch<T, 8, 6, 32>(p, s);
-    else if (units <= 32 * 8) norm_launch<T, 8, 8, 32>(p, s);
-    else if (units <= 32 * 10) norm_launch<T, 8, 10, 32>(p, s);
-    else if (units <= 128 * 4) norm_launch<T, 8, 4, 128>(p, s);
-    else if (units <= 128 * 7) norm_launch<T, 8, 7, 128>(p, s);
-    else if (units <= 128 * 10) norm_launch<T, 8, 10, 128>(p, s);
-    else if (units <= 512 * 5) norm_launch<T, 8, 5, 512>(p, s);
-    else norm_launch<T, 8, 10, 512>(p, s);
-  } else if (p.D <= 32 * 10) {
-    norm_launch<T, 1, 10, 32>(p, s);
-  } else if (p.D <= 128 * 10) {
-    norm_launch<T, 1, 10, 128>(p, s);
-  } else if (p.D <= 128 * 20) {
-    norm_launch<T, 1, 20, 128>(p, s);
-  } else {
-    rms_norm_long_kernel<T><<<static_cast<unsigned>(p.rows), 512, 0, s>>>(p);
-  }
+  if (mode == kNormVec && p.D <= kNormMaxVec) return launch_norm_units<T, kNormVec>(p, p.D / 8, s);
+  if (mode == kNormShift && p.D > 64 && p.D <= 20480 - 14) return launch_norm_units<T, kNormShift>(p, (p.D + 14) / 8, s);
+  if (p.D <= 8) return norm_launch<T, kNormOne, 2, 4>(p, s);
+  if (p.D <= 64) return norm_launch<T, kNormOne, 4, 16>(p, s);
+  if (p.D <= 32 * 10) return norm_launch<T, kNormOne, 10, 32>(p, s);
+  if (p.D <= 128 * 10) return norm_launch<T, kNormOne, 10, 128>(p, s);
+  if (p.D <= 128 * 20) return norm_launch<T, kNormOne, 20, 128>(p, s);
+  rms_norm_long_kernel<T><<<static_cast<unsigned>(p.rows), 512, 0, s>>>(p);
   return launch_status();
 }
 
@@ -1158,8 +1161,9 @@ safe_status safe_rms_norm(const void* x, int x_full, const void* res, const int3
       if (overlap(q, n_rows, in[i], len[i]) || overlap(q_scales, sb, in[i], len[i])) return SAFE_ERR_INVALID_ARG;
     if (overlap(q, n_rows, q_scales, sb)) return SAFE_ERR_INVALID_ARG;
   }
-  const bool vec = D % 8 == 0 && aligned_to(x, 16) && aligned_to(res, 16) && aligned_to(w, 16) && aligned_to(h, 16) &&
-                   aligned_to(y, 16);
+  const bool aligned = aligned_to(x, 16) && aligned_to(res, 16) && aligned_to(h, 16) && aligned_to(y, 16);
+  const bool vec = aligned && D % 8 == 0 && aligned_to(w, 16);
+  const int mode = vec ? kNormVec : aligned && S == nullptr ? kNormShift : kNormOne;
   if (q != nullptr && (D % 32 != 0 || !vec)) return SAFE_ERR_INVALID_ARG;
   if (q != nullptr && D > kNormMaxVec) return SAFE_ERR_UNSUPPORTED;
   p.x = x;
@@ -1179,9 +1183,9 @@ safe_status safe_rms_norm(const void* x, int x_full, const void* res, const int3
   p.ct = q != nullptr ? mx_tiles(D, SAFE_MXFP8) : 0;
   p.rows_pad = q != nullptr ? (p.rows + 127) / 128 * 128 : p.rows;
   switch (dtype) {
-    case SAFE_F32: return launch_norm<float>(p, vec, as_stream(stream));
-    case SAFE_F16: return launch_norm<__half>(p, vec, as_stream(stream));
-    default: return launch_norm<__nv_bfloat16>(p, vec, as_stream(stream));
+    case SAFE_F32: return launch_norm<float>(p, mode, as_stream(stream));
+    case SAFE_F16: return launch_norm<__half>(p, mode, as_stream(stream));
+    default: return launch_norm<__nv_bfloat16>(p, mode, as_stream(stream));
   }
 }
 
