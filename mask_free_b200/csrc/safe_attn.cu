@@ -482,6 +482,7 @@ bool apart(const View4& s, const View4& t, size_t e) {
   return false;
 }
 constexpr int kMxMaxD = 1 << 20;  // keeps the positions of 128 rows below 2^31
+constexpr int64_t kMxMaxRows = INT_MAX - 255;  // and the rows of the last, partial tile
 int mx_block(int fmt) { return fmt == SAFE_NVFP4 ? 16 : 32; }
 // Scale tiles along a row of D elements.
 int mx_tiles(int D, int fmt) { return (D / mx_block(fmt) + 3) / 4; }
@@ -1269,7 +1270,7 @@ safe_status safe_mx_quantize(const void* X, int dtype, const int32_t* S, int k, 
   if (!aligned16(X) || !aligned16(data) || !aligned16(scales) || !aligned_to(S, 4)) return SAFE_ERR_INVALID_ARG;
   if (!sizes_ok(B, N, 1) || (S != nullptr && (k < 1 || k > N)) || D < 32 || D % 32 != 0) return SAFE_ERR_INVALID_ARG;
   if (!mx_factor_ok(fmt, g)) return SAFE_ERR_INVALID_ARG;
-  if (D > kMxMaxD) return SAFE_ERR_UNSUPPORTED;
+  if (D > kMxMaxD || static_cast<int64_t>(B) * (S != nullptr ? k : N) > kMxMaxRows) return SAFE_ERR_UNSUPPORTED;
   MxQuantParams p{};
   p.X = X;
   p.S = S;
@@ -1301,7 +1302,7 @@ safe_status safe_mx_dequantize(const void* data, const void* scales, int fmt, fl
   if (float_size(dtype) == 0) return SAFE_ERR_UNSUPPORTED;
   if (!aligned16(data) || !aligned16(scales) || !aligned16(Y)) return SAFE_ERR_INVALID_ARG;
   if (rows < 1 || rows > INT_MAX || D < 32 || D % 32 != 0 || !mx_factor_ok(fmt, g)) return SAFE_ERR_INVALID_ARG;
-  if (D > kMxMaxD) return SAFE_ERR_UNSUPPORTED;
+  if (D > kMxMaxD || rows > kMxMaxRows) return SAFE_ERR_UNSUPPORTED;
   const size_t db = static_cast<size_t>(rows) * (fmt == SAFE_MXFP8 ? D : D / 2);
   const size_t yb = static_cast<size_t>(rows) * D * float_size(dtype);
   if (overlap(Y, yb, data, db) || overlap(Y, yb, scales, safe_mx_scale_bytes(rows, D, fmt))) return SAFE_ERR_INVALID_ARG;
@@ -1324,7 +1325,7 @@ safe_status safe_mx_dequantize(const void* data, const void* scales, int fmt, fl
 }
 
 size_t safe_mx_linear_workspace_bytes(int64_t rows, int d_in, int d_out, int fmt) {
-  if (fmt < SAFE_MXFP8 || fmt > SAFE_NVFP4 || rows < 1 || rows > INT_MAX || d_in < 64 || d_in % 32 != 0 || d_out < 8 ||
+  if (fmt < SAFE_MXFP8 || fmt > SAFE_NVFP4 || rows < 1 || rows > kMxMaxRows || d_in < 64 || d_in % 32 != 0 || d_out < 8 ||
       d_out % 8 != 0)
     return 0;
   return mx_linear_plan(rows, d_out, fmt == SAFE_MXFP8 ? d_in : d_in / 2, mx_linear_pairs(fmt), true).part_bytes;
@@ -1338,6 +1339,7 @@ safe_status safe_mx_linear(const void* X, const void* X_scales, const void* Wt, 
     return SAFE_ERR_INVALID_ARG;
   if (fmt < SAFE_MXFP8 || fmt > SAFE_NVFP4 || !std::isnormal(alpha) || (act != 0 && act != 1)) return SAFE_ERR_INVALID_ARG;
   if (rows < 1 || rows > INT_MAX || d_in < 64 || d_in % 32 != 0 || d_out < 8 || d_out % 8 != 0) return SAFE_ERR_INVALID_ARG;
+  if (rows > kMxMaxRows) return SAFE_ERR_UNSUPPORTED;
   const int row_bytes = fmt == SAFE_MXFP8 ? d_in : d_in / 2;
   const size_t yb = static_cast<size_t>(rows) * d_out * 2;
   if (overlap(Y, yb, X, static_cast<size_t>(rows) * row_bytes) ||

@@ -716,21 +716,27 @@ def rms_norm(x, w=None, residual=None, S=None, eps=1e-6, x_compact=False, quant=
 class RopeTable:
     """The frequencies of rotary positions (made by rope_table): `freq` [r / 2]
     int64 in 2^-64 turns, `sections` the pairs of each position axis, `m` the
-    factor on the rotated elements."""
+    factor on the rotated elements. Checked once, here: its parts cannot be
+    exchanged afterwards."""
 
-    __slots__ = ("freq", "sections", "m", "r", "_sections", "_freq_ptr")
+    __slots__ = ("_freq", "_sections", "_m", "_r", "_counts", "_freq_ptr")
 
     def __init__(self, freq: torch.Tensor, sections: Sequence[int], m: float = 1.0):
         _need(freq, "freq", torch.int64, 1)
-        self.sections = tuple(int(n) for n in sections)
-        self.r = 2 * freq.shape[0]
-        if not 1 <= len(self.sections) <= 3 or min(self.sections) < 0 or 2 * sum(self.sections) != self.r or self.r < 2:
-            raise ValueError(f"sections must be 1 to 3 counts that share out {self.r // 2} pairs, got {self.sections}")
+        self._sections = tuple(int(n) for n in sections)
+        self._r = 2 * freq.shape[0]
+        if not 1 <= len(self._sections) <= 3 or min(self._sections) < 0 or 2 * sum(self._sections) != self._r or self._r < 2:
+            raise ValueError(f"sections must be 1 to 3 counts that share out {self._r // 2} pairs, got {self._sections}")
         if not math.isfinite(m):
             raise ValueError(f"m must be finite, got {m}")
-        self.freq, self.m = freq, float(m)
-        self._sections = (ctypes.c_int32 * len(self.sections))(*self.sections)
+        self._freq, self._m = freq, float(m)
+        self._counts = (ctypes.c_int32 * len(self._sections))(*self._sections)
         self._freq_ptr = ctypes.cast(freq.data_ptr(), _i64p)
+
+    freq = property(lambda self: self._freq)
+    sections = property(lambda self: self._sections)
+    m = property(lambda self: self._m)
+    r = property(lambda self: self._r)
 
 
 def rope_frequencies(r: int, base: float = 10000.0, sections: Optional[Sequence[int]] = None, kind: str = "none",
@@ -814,13 +820,13 @@ def rope(q, k, table: RopeTable, pos=None, S=None, interleaved=False, inplace=Fa
     if not _on_device(q) or q.dim() != 4:
         raise ValueError(f"q must be a CUDA tensor of 4 dims, got {tuple(q.shape)} on {q.device}")
     B, R, _, d = q.shape
-    dev, dtype, axes, r = q.device, q.dtype, len(table.sections), table.r
+    dev, dtype, axes, r = q.device, q.dtype, len(table._sections), table._r
     H, qs = _heads(q, "q", dtype, B, R, d, dev)
     Hk, ks, kp = 0, None, None
     if k is not None:
         Hk, ks = _heads(k, "k", dtype, B, R, d, dev)
         kp = k.data_ptr()
-    if table.freq.device != dev:
+    if table._freq.device != dev:
         raise ValueError(f"table must be on {dev}")
     if r > d:
         raise ValueError(f"the table turns {r} elements, heads have {d}")
@@ -871,7 +877,7 @@ def rope(q, k, table: RopeTable, pos=None, S=None, interleaved=False, inplace=Fa
             if n != Hk:
                 raise ValueError(f"out[1] must have {Hk} heads, got {n}")
     _run("safe_rope", dev, q.data_ptr(), qs, oq.data_ptr(), oqs, H, kp, ks, None if k is None else ok.data_ptr(), oks, Hk, dt,
-         table._freq_ptr, table._sections, axes, pp, batched, sp, B, N, R, d, r, 1 if interleaved else 0, table.m)
+         table._freq_ptr, table._counts, axes, pp, batched, sp, B, N, R, d, r, 1 if interleaved else 0, table._m)
     return oq, ok
 
 

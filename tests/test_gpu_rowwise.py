@@ -5,6 +5,9 @@ output type plus the fp32 roundings of the kernel's own sums and products.
 Outputs lie inside larger buffers whose other bytes must not change."""
 
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -179,6 +182,18 @@ def test_norm_updates_the_stream_in_place():
     assert ops.device_status() == 0
 
 
+@pytest.mark.parametrize("D", [64, 2304])
+def test_norm_with_both_outputs(D):
+    # the C entry point writes y and its 8-bit form in one call
+    x, w = randn((1, 130, D), 1, bf16).to(DEV), randn((D,), 2).to(DEV)
+    y, m = torch.empty_like(x), ops.rms_norm(x, w, quant="mxfp8")
+    q, sc = torch.zeros_like(m.data.view(torch.uint8)), torch.zeros_like(m.scales)
+    st = ops.lib().safe_rms_norm(x.data_ptr(), 0, None, None, 0, w.data_ptr(), 1e-6, None, 0, y.data_ptr(), q.data_ptr(),
+                                 sc.data_ptr(), 4, 1, 130, D, torch.cuda.current_stream().cuda_stream)
+    assert st == ops.SAFE_OK and torch.equal(y, ops.rms_norm(x, w))
+    assert torch.equal(q, m.data.view(torch.uint8)) and torch.equal(sc, m.scales)
+
+
 @pytest.mark.parametrize("D", [64, 63, 41000])
 def test_norm_bad_rows_are_flagged_and_zero(D):
     x, r = randn((1, 5, D), 1, bf16).to(DEV), randn((1, 9, D), 2, bf16).to(DEV)
@@ -274,6 +289,43 @@ def test_rope_parity(dtype, B, N, k, H, Hk, d, r, axes, far):
         assert iq is gq and torch.equal(gq, oq) and torch.equal(gk, ok)
         if fused:
             assert torch.equal(dq[:, :, H + Hk:].cpu(), qkv[:, :, H + Hk:])
+    assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,H,Hk,d,r,interleaved", [
+    (bf16, 24, 8, 96, 96, False), (bf16, 24, 24, 96, 64, True), (f16, 12, 6, 128, 128, False), (bf16, 36, 0, 64, 64, True),
+    (f16, 3, 2, 512, 512, False), (bf16, 1, 1, 1024, 1024, True), (f32, 9, 3, 96, 96, True)])
+def test_rope_of_many_tokens(dtype, H, Hk, d, r, interleaved):
+    # enough tokens for the ring of bulk copies: rows S, positions of each
+    # sample, fused views, in place; sampled rows against the oracle
+    B, N, k = 2, 3000, 2700
+    sec = [r // 2 - r // 8, r // 8]
+    tab, (f, m) = ops.rope_table(r, sections=sec), ops.rope_frequencies(r, sections=sec)
+    S, rng = rows(B, N, k, 1), np.random.default_rng(2)
+    pos = rng.integers(-1000, 1000000, size=(B, N, 2)).astype(np.int32)
+    pick = np.unique(np.r_[0, 1, k - 2, k - 1, rng.choice(k, 60, replace=False)])
+    at = np.stack([pos[b, S[b, pick]] for b in range(B)])
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    qkv = torch.randn((B, k, H + 2 * max(Hk, 1), d), generator=gen, device=DEV).to(dtype)
+    before = qkv.clone()
+    q, kk = qkv[:, :, :H], qkv[:, :, H:H + Hk] if Hk else None
+    pk = torch.from_numpy(pick).to(DEV)
+    want = [O.rope(to64(t[:, pk]), f, sec, at, interleaved, m) for t in (q, kk) if t is not None]
+    new = ops.rope(q, kk, tab, pos=dev(pos), S=dev(S), interleaved=interleaved)
+    for t, got, ref in zip((q, kk), new, want):
+        rope_check(got[:, pk], t[:, pk], ref, dtype, r, m)
+    buf, o = guarded((B, k, H, d), dtype)
+    ops.rope(q, kk, tab, pos=dev(pos), S=dev(S), interleaved=interleaved, out=(o, None))
+    assert torch.equal(o, new[0]) and untouched(buf) and torch.equal(qkv, before)
+    ops.rope(q, kk, tab, pos=dev(pos), S=dev(S), interleaved=interleaved, inplace=True)
+    assert torch.equal(q, new[0]) and (kk is None or torch.equal(kk, new[1]))
+    assert torch.equal(qkv[:, :, H + Hk:], before[:, :, H + Hk:])
+    bad = dev(S).clone()
+    bad[1, 17] = N
+    got, _ = ops.rope(before[:, :, :H], None, tab, pos=dev(pos), S=bad, interleaved=interleaved)
+    assert ops.device_status() == FLAG
+    bad[1, 17] = 0
+    assert torch.equal(got, ops.rope(before[:, :, :H], None, tab, pos=dev(pos), S=bad, interleaved=interleaved)[0])
     assert ops.device_status() == 0
 
 
@@ -488,6 +540,22 @@ def test_mx_linear_parity(fmt, M, d_in, d_out, act, with_bias):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4", "nvfp4"])
+@pytest.mark.parametrize("d_in", [64, 96, 192, 288, 512])
+def test_mx_linear_short_rows_many_tiles(fmt, d_in):
+    # one to four stages of K a tile, several tiles to a CTA pair; Y aligned to
+    # 16 bytes only
+    M, d_out = 6000, 2304
+    X, mX = operand(M, d_in, fmt, 11)
+    W, mW = operand(d_out, d_in, fmt, 12)
+    bias = np.random.default_rng(3).normal(size=d_out).astype(np.float32) * 100
+    pick = np.random.default_rng(0).choice(M, 300, replace=False)
+    buf, out = guarded((M, d_out), bf16, pad=272)
+    y = ops.mx_linear(mX, mW, dev(bias), out=out)
+    linear_check(y[torch.from_numpy(pick).to(DEV)], X[pick], W, bias, "none")
+    assert untouched(buf, pad=272) and torch.equal(ops.mx_linear(mX, mW, dev(bias)), y) and ops.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4", "nvfp4"])
 def test_mx_linear_many_tiles_and_nan_rows(fmt):
     # several tiles to a CTA pair; a NaN row stays in its row
     M, d_in, d_out = 2500, 256, 4608
@@ -645,6 +713,31 @@ def test_streams_and_graphs(fmt, k):
         for o in outs:
             assert all(torch.equal(a, b) for a, b in zip(o, want[i]))
     assert ops.device_status() == 0
+
+
+def test_first_calls_inside_a_capture():
+    # a process whose first calls are captured: nothing in them needs a stream
+    code = """
+import torch
+from mask_free_b200 import ops
+x = torch.randn((1, 300, 256), device="cuda").to(torch.bfloat16)
+w = torch.randn((192, 256), device="cuda").to(torch.bfloat16)
+tab = ops.rope_table(64)
+ops.lib()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y = ops.rms_norm(x, quant="mxfp8")
+    z = ops.mx_linear(y, ops.mx_quantize(w, "mxfp8"), act="gelu_tanh")
+    q, _ = ops.rope(z.view(1, 300, 3, 64), None, tab)
+g.replay()
+torch.cuda.synchronize()
+z = ops.mx_linear(ops.rms_norm(x, quant="mxfp8"), ops.mx_quantize(w, "mxfp8"), act="gelu_tanh")
+assert torch.equal(q, ops.rope(z.view(1, 300, 3, 64), None, tab)[0]) and ops.device_status() == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_long_tensors():
