@@ -154,6 +154,29 @@ __device__ __forceinline__ __half from_float<__half>(float x) { return __float2h
 template <>
 __device__ __forceinline__ float from_float<float>(float x) { return x; }
 
+// ---------------------------------------------------------------- arithmetic
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if one of them is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Both factors of each of four pairs of v times m.
+__device__ __forceinline__ void scale8(const float* v, float m, float* r) {
+  const uint64_t mm = f2_pack(m, m);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) f2_unpack(f2_mul(f2_pack(v[i], v[i + 1]), mm), r[i], r[i + 1]);
+}
+
 // ---------------------------------------------------------------- conversions
 // Four floats to e4m3 / eight to e2m1 (nearest, ties to even, at most the
 // largest finite value); element 0 in the lowest bits.
@@ -163,7 +186,9 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
   return static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
 }
-__device__ __forceinline__ uint32_t e2m1x8(const float* v, float m) {
+__device__ __forceinline__ uint32_t e2m1x8(const float* v, float m) {  // of v m
+  float f[8];
+  scale8(v, m, f);
   uint32_t r;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -172,9 +197,13 @@ __device__ __forceinline__ uint32_t e2m1x8(const float* v, float m) {
       "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
       "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
       : "=r"(r)
-      : "f"(v[0] * m), "f"(v[1] * m), "f"(v[2] * m), "f"(v[3] * m), "f"(v[4] * m), "f"(v[5] * m), "f"(v[6] * m),
-        "f"(v[7] * m));
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
   return r;
+}
+__device__ __forceinline__ uint2 e4m3x8(const float* v, float m) {  // of v m
+  float f[8];
+  scale8(v, m, f);
+  return make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
 }
 // The value of an e4m3 byte (0x7f and 0xff are NaN).
 __device__ __forceinline__ float e4m3_value(uint32_t byte) {
@@ -233,7 +262,7 @@ __device__ __forceinline__ float e2m1_border(uint32_t c) {
 }
 
 // Eight elements of an nvfp4 block with scale value s (inv ~ 1 / (s g) within
-// 2^-22): nearest e2m1 of v / (s g), exactly, by the same two conversions;
+// 3 2^-24; the product with v and that with 1 -+ 2^-21 add 2^-24 each): nearest e2m1 of v / (s g), exactly, by the same two conversions;
 // where they differ, the element's border's product border * s (7 bits) decides
 // by the sign of one fma, and a tie goes to the even code. (Ties are common
 // where g is a short number: bf16 inputs have 8 bits. So the loop takes only
@@ -269,10 +298,10 @@ __device__ __forceinline__ uint32_t amax16(const Raw8<__half>& a, const Raw8<__h
   return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(amax16_bits(a.a, b.a)))));
 }
 __device__ __forceinline__ uint32_t amax16(const Raw8<float>&, const Raw8<float>&, const float* v) {
-  uint32_t m = 0;
+  float m = 0.f;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
-  return m;
+  for (int e = 0; e < 16; ++e) m = max_nan(m, fabsf(v[e]));
+  return __float_as_uint(m);
 }
 
 // ---------------------------------------------------------------- rows in groups of 128
@@ -350,7 +379,7 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const MxQuantParams p)
     if constexpr (kFmt == kNvFp4) {
       byte = nvfp4_scale(amax, p.g, p.inv6g);
       const float s = e4m3_value(byte);
-      const float inv = byte == 0 || byte == 0x7fu ? 0.f : __frcp_rn(s * p.g);
+      const float inv = byte == 0 || byte == 0x7fu ? 0.f : rcp_approx(s * p.g);
       out[0] = nvfp4_elements(v, s, p.g, inv);
       out[1] = nvfp4_elements(v + 8, s, p.g, inv);
     } else {
@@ -361,9 +390,11 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const MxQuantParams p)
         out[0] = e2m1x8(v, inv);
         out[1] = e2m1x8(v + 8, inv);
       } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          out[e] = e4m3x4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv, v[4 * e + 3] * inv);
+        const uint2 lo = e4m3x8(v, inv), hi = e4m3x8(v + 8, inv);
+        out[0] = lo.x;
+        out[1] = lo.y;
+        out[2] = hi.x;
+        out[3] = hi.y;
       }
     }
     // this row's word of scales; those past the row or the matrix are zero

@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const N
         a[i].get(v + 8 * i);
         b[i].get(f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[8 * i + e] += f[e];
+        for (int e = 0; e < 8; e += 2)
+          f2_unpack(f2_add(f2_pack(v[8 * i + e], v[8 * i + e + 1]), f2_pack(f[e], f[e + 1])), v[8 * i + e], v[8 * i + e + 1]);
       }
     } else {
 #pragma unroll
@@ -158,8 +159,20 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const N
     }
   }
   float ss = 0.f;
+  if constexpr (VEC == 8) {
+    uint64_t s2 = f2_pack(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < NV * VEC; ++i) ss = fmaf(v[i], v[i], ss);
+    for (int i = 0; i < NV * 8; i += 2) {
+      const uint64_t x2 = f2_pack(v[i], v[i + 1]);
+      s2 = f2_fma(x2, x2, s2);
+    }
+    float lo, hi;
+    f2_unpack(s2, lo, hi);
+    ss = lo + hi;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) ss = fmaf(v[i], v[i], ss);
+  }
   ss = row_sum<TPR>(ss, part);
   const float rstd = ok ? 1.f / sqrtf(ss / static_cast<float>(p.D) + p.eps) : 0.f;
 
@@ -176,8 +189,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const N
       continue;
     } else {
       float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = v[8 * i + e] * rstd;
+      scale8(v + 8 * i, rstd, f);
       const int at = 8 * u - shift;  // the unit's first element
       if (kMode == kNormVec || (at >= 0 && at + 8 <= p.D)) {
         if (in && h_write) store8(h + at, v + 8 * i);
@@ -185,8 +197,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const N
           if constexpr (kMode == kNormVec) {
             const float4 w0 = __ldg(reinterpret_cast<const float4*>(p.w) + 2 * u);
             const float4 w1 = __ldg(reinterpret_cast<const float4*>(p.w) + 2 * u + 1);
-            f[0] *= w0.x; f[1] *= w0.y; f[2] *= w0.z; f[3] *= w0.w;
-            f[4] *= w1.x; f[5] *= w1.y; f[6] *= w1.z; f[7] *= w1.w;
+            f2_unpack(f2_mul(f2_pack(f[0], f[1]), f2_pack(w0.x, w0.y)), f[0], f[1]);
+            f2_unpack(f2_mul(f2_pack(f[2], f[3]), f2_pack(w0.z, w0.w)), f[2], f[3]);
+            f2_unpack(f2_mul(f2_pack(f[4], f[5]), f2_pack(w1.x, w1.y)), f[4], f[5]);
+            f2_unpack(f2_mul(f2_pack(f[6], f[7]), f2_pack(w1.z, w1.w)), f[6], f[7]);
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] *= __ldg(p.w + at + e);
@@ -209,9 +223,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const N
         if (p.q != nullptr) {
           // blocks of 32: four threads; a word of scales: sixteen (D is a
           // multiple of 32, so a block is inside the row or past its end)
-          uint32_t amax = 0;
+          float top = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(f[e]) & 0x7fffffffu);
+          for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(f[e]));
+          uint32_t amax = __float_as_uint(top);
           amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
           amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
           float inv;
@@ -223,8 +238,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const N
           if (in && row < p.rows_pad) {
             if (live)
               *reinterpret_cast<uint2*>(p.q + row * p.D + u * 8) =
-                  make_uint2(e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                             e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+                  e4m3x8(f, inv);
             if ((t & 15) == 0) *reinterpret_cast<uint32_t*>(p.q_scales + mx_scale_at(row, u >> 2, p.ct)) = word;
           }
         }
