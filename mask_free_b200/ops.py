@@ -534,7 +534,13 @@ def _on(dev: torch.device, fn, *args):
 def _run(name: str, dev: torch.device, *args):
     """Call entry point `name` on `dev` (which need not be the current device)
     with that device's current stream as the last argument."""
-    st = _on(dev, getattr(lib(), name), *args, _stream() if dev.index is None else _raw_stream(dev.index))
+    fn, idx = getattr(lib(), name), dev.index
+    if idx is None:
+        st = fn(*args, _stream())
+    elif idx == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(idx))
+    else:
+        st = _on(dev, fn, *args, _raw_stream(idx))
     if st != SAFE_OK:
         raise SafeError(name, st)
 
@@ -593,7 +599,7 @@ class MxTensor:
     factor of the whole matrix (nvfp4; 1 otherwise). Checked once, here: its
     parts cannot be exchanged afterwards."""
 
-    __slots__ = ("_data", "_scales", "_fmt", "_scale")
+    __slots__ = ("_data", "_scales", "_fmt", "_scale", "_rows", "_D")
 
     def __init__(self, data: torch.Tensor, scales: torch.Tensor, fmt: str, scale: float = 1.0):
         if fmt not in _FORMATS:
@@ -603,9 +609,14 @@ class MxTensor:
             raise ValueError("data must be a tensor of at least 2 dims")
         if not (_on_device(data) and data.dtype is want and data.is_contiguous()):
             _need(data, "data", want, data.dim())
-        rows, D = _mx_rows(data, fmt)
+        w, n = data.shape[-1], data.numel()
+        D = w if fmt == "mxfp8" else 2 * w
+        if D < 32 or D % 32 or n == 0:
+            raise ValueError(f"rows of a microscaled matrix have a multiple of 32 elements, got {tuple(data.shape)}")
+        rows = n // w
         _check_tensor(scales, "scales", torch.uint8, (mx_scale_bytes(rows, D, fmt),), data.device)
         self._data, self._scales, self._fmt, self._scale = data, scales, fmt, _factor(fmt, scale)
+        self._rows, self._D = rows, D
 
     data = property(lambda self: self._data)
     scales = property(lambda self: self._scales)
@@ -615,20 +626,11 @@ class MxTensor:
     @property
     def shape(self) -> Tuple[int, ...]:
         """The shape of the values that the matrix stands for."""
-        return (*self.data.shape[:-1], _mx_rows(self.data, self.fmt)[1])
+        return (*self._data.shape[:-1], self._D)
 
     @property
     def device(self) -> torch.device:
-        return self.data.device
-
-
-def _mx_rows(data: torch.Tensor, fmt: str):
-    """(rows, D) of a microscaled matrix's elements."""
-    w = data.shape[-1]
-    D = w if fmt == "mxfp8" else 2 * w
-    if D < 32 or D % 32 or data.numel() == 0:
-        raise ValueError(f"rows of a microscaled matrix have a multiple of 32 elements, got {tuple(data.shape)}")
-    return data.numel() // w, D
+        return self._data.device
 
 
 def mx_scale_bytes(rows: int, D: int, fmt: str) -> int:
@@ -645,10 +647,13 @@ def _mx_out(out, lead, D: int, fmt: str, scale: float, like) -> MxTensor:
     contents, or the given one checked."""
     if out is None:
         m = MxTensor.__new__(MxTensor)  # made to fit: nothing to check
-        m._data = like.new_empty((*lead, D) if fmt == "mxfp8" else (*lead, D // 2),
-                                 dtype=torch.float8_e4m3fn if fmt == "mxfp8" else torch.uint8)
-        m._scales = like.new_empty(mx_scale_bytes(math.prod(lead), D, fmt), dtype=torch.uint8)
-        m._fmt, m._scale = fmt, scale
+        rows = math.prod(lead)
+        if fmt == "mxfp8":
+            m._data = like.new_empty((*lead, D), dtype=torch.float8_e4m3fn)
+        else:
+            m._data = like.new_empty((*lead, D // 2), dtype=torch.uint8)
+        m._scales = like.new_empty(mx_scale_bytes(rows, D, fmt), dtype=torch.uint8)
+        m._fmt, m._scale, m._rows, m._D = fmt, scale, rows, D
         return m
     if not isinstance(out, MxTensor) or out.fmt != fmt or out.shape != (*lead, D) or out.device != like.device:
         raise ValueError(f"out must be an MxTensor {fmt} of shape {(*lead, D)} on {like.device}")
@@ -707,7 +712,7 @@ def rms_norm(x, w=None, residual=None, S=None, eps=1e-6, x_compact=False, quant=
         if D % 32:
             raise ValueError(f"an 8-bit output needs D a multiple of 32, got {D}")
         y = _mx_out(out, (B, R), D, quant, 1.0, x)
-        yp, qp, sp = None, y.data.data_ptr(), y.scales.data_ptr()
+        yp, qp, sp = None, y._data.data_ptr(), y._scales.data_ptr()
     _run("safe_rms_norm", dev, x.data_ptr(), 1 if full else 0, _ptr(residual), _ptr(S), k, _ptr(w), eps, _ptr(h),
          1 if update and k else 0, yp, qp, sp, dt, B, N, D)
     return y if residual is None else (y, h)
@@ -819,9 +824,9 @@ def rope(q, k, table: RopeTable, pos=None, S=None, interleaved=False, inplace=Fa
         raise ValueError("table must be a RopeTable")
     if not _on_device(q) or q.dim() != 4:
         raise ValueError(f"q must be a CUDA tensor of 4 dims, got {tuple(q.shape)} on {q.device}")
-    B, R, _, d = q.shape
+    B, R, H, d = q.shape
     dev, dtype, axes, r = q.device, q.dtype, len(table._sections), table._r
-    H, qs = _heads(q, "q", dtype, B, R, d, dev)
+    qs = None if q.is_contiguous() else _heads(q, "q", dtype, B, R, d, dev)[1]
     Hk, ks, kp = 0, None, None
     if k is not None:
         Hk, ks = _heads(k, "k", dtype, B, R, d, dev)
@@ -862,7 +867,7 @@ def rope(q, k, table: RopeTable, pos=None, S=None, interleaved=False, inplace=Fa
         oq, ok = (None, None) if out is None else out
         oqs = oks = None
         if oq is None:
-            oq = _out_like(None, "", q, dtype, q.shape)
+            oq = torch.empty_like(q) if qs is None else q.new_empty((B, R, H, d))
         else:
             n, oqs = _heads(oq, "out[0]", dtype, B, R, d, dev)
             if n != H:
@@ -871,7 +876,7 @@ def rope(q, k, table: RopeTable, pos=None, S=None, interleaved=False, inplace=Fa
             if ok is not None:
                 raise ValueError("out[1] needs k")
         elif ok is None:
-            ok = _out_like(None, "", k, dtype, k.shape)
+            ok = torch.empty_like(k) if ks is None else k.new_empty((B, R, Hk, d))
         else:
             n, oks = _heads(ok, "out[1]", dtype, B, R, d, dev)
             if n != Hk:
@@ -917,7 +922,7 @@ def mx_quantize(x, fmt: str, S=None, scale: float = 1.0, out=None) -> MxTensor:
             raise ValueError("S needs x of 3 dims")
         R = k = _rows_of(S, B, N, dev)
     m = _mx_out(out, (B, R) if nd == 3 else (N,), D, fmt, g, x)
-    _run("safe_mx_quantize", dev, x.data_ptr(), dt, _ptr(S), k, code, g, m.data.data_ptr(), m.scales.data_ptr(), B, N, D)
+    _run("safe_mx_quantize", dev, x.data_ptr(), dt, _ptr(S), k, code, g, m._data.data_ptr(), m._scales.data_ptr(), B, N, D)
     return m
 
 
@@ -927,11 +932,10 @@ def mx_dequantize(m: MxTensor, dtype=torch.bfloat16, out=None):
         raise ValueError("m must be an MxTensor")
     if dtype not in _FLOATS:
         raise ValueError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
-    rows, D = _mx_rows(m.data, m.fmt)
-    dev = m.device
-    out = _out_like(out, "out", m.scales, dtype, (*m.data.shape[:-1], D))
-    _run("safe_mx_dequantize", dev, m.data.data_ptr(), m.scales.data_ptr(), _FORMATS[m.fmt], m.scale, out.data_ptr(),
-         _FLOATS[dtype], rows, D)
+    data, D = m._data, m._D
+    out = _out_like(out, "out", m._scales, dtype, (*data.shape[:-1], D))
+    _run("safe_mx_dequantize", data.device, data.data_ptr(), m._scales.data_ptr(), _FORMATS[m._fmt], m._scale, out.data_ptr(),
+         _FLOATS[dtype], m._rows, D)
     return out
 
 
@@ -950,30 +954,30 @@ def mx_linear(X: MxTensor, W: MxTensor, bias=None, act="none", out=None, ws=None
     one when None; False: every tile whole)."""
     if not isinstance(X, MxTensor) or not isinstance(W, MxTensor):
         raise ValueError("X and W must be MxTensors")
-    if X.fmt != W.fmt:
-        raise ValueError(f"X is {X.fmt}, W is {W.fmt}: both operands must have one format")
-    rows, d_in = _mx_rows(X.data, X.fmt)
-    d_out, dw = W.data.shape[0], _mx_rows(W.data, W.fmt)[1]
-    dev = X.device
-    if W.data.dim() != 2 or dw != d_in or W.device != dev:
+    fmt, x, w = X._fmt, X._data, W._data
+    if fmt != W._fmt:
+        raise ValueError(f"X is {fmt}, W is {W._fmt}: both operands must have one format")
+    rows, d_in, d_out, dev = X._rows, X._D, W._rows, x.device
+    if w.dim() != 2 or W._D != d_in or w.device != dev:
         raise ValueError(f"W must be [d_out, {d_in}] on {dev}, got {W.shape} on {W.device}")
     if bias is not None:
         _check_tensor(bias, "bias", torch.float32, (d_out,), dev)
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
-    alpha = X.scale * W.scale
+    alpha = X._scale * W._scale
     if not 2.0 ** -126 <= abs(alpha) < 2.0 ** 128:
         raise ValueError(f"the product of the operands' factors is out of range: {alpha}")
-    out = _out_like(out, "out", X.scales, torch.bfloat16, (*X.data.shape[:-1], d_out))
-    code, wp, wb = _FORMATS[X.fmt], None, 0
+    out = _out_like(out, "out", X._scales, torch.bfloat16, (*x.shape[:-1], d_out))
+    code, wp, wb = _FORMATS[fmt], None, 0
     if ws is None:
-        wb = _on(dev, lib().safe_mx_linear_workspace_bytes, rows, d_in, d_out, code)
-        if wb:
-            ws = X.scales.new_empty(wb)
-            wp = ws.data_ptr()
+        if x.shape[-1] > 1536:  # up to 12 stages of 128 bytes a split saves less than it costs
+            wb = _on(dev, lib().safe_mx_linear_workspace_bytes, rows, d_in, d_out, code)
+            if wb:
+                ws = X._scales.new_empty(wb)
+                wp = ws.data_ptr()
     elif ws is not False:
         _need(ws, "ws", torch.uint8, 1, device=dev)
         wp, wb = ws.data_ptr(), ws.numel()
-    _run("safe_mx_linear", dev, X.data.data_ptr(), X.scales.data_ptr(), W.data.data_ptr(), W.scales.data_ptr(), code,
-         alpha, _ptr(bias), _ACTS[act], out.data_ptr(), rows, d_in, d_out, wp, wb)
+    _run("safe_mx_linear", dev, x.data_ptr(), X._scales.data_ptr(), w.data_ptr(), W._scales.data_ptr(), code, alpha,
+         _ptr(bias), _ACTS[act], out.data_ptr(), rows, d_in, d_out, wp, wb)
     return out
