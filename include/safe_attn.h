@@ -351,7 +351,9 @@ safe_status safe_gather_linear(const void* X, const int32_t* S, int k, const voi
 /*
  * Root-mean-square norm of rows with the residual's addition: what lies
  * between the branches of the block B (Eq. (18)) and of its row-selective
- * form B^S (Eq. (15)). For every output row (b, r):
+ * form B^S (Eq. (15)). The paper does not name the block's norm; it is
+ * row-wise, so it commutes with the row selection of Eq. (13). For every
+ * output row (b, r):
  *   h = x + res            (res == NULL: h = x)
  *   y = h / sqrt(mean(h^2) + eps) * w
  * S == NULL: R = N rows in order, k ignored. Else R = k, row r belongs to
@@ -382,7 +384,8 @@ safe_status safe_rms_norm(const void* x, int x_full, const void* res, const int3
                           int D, void* stream);
 
 /*
- * Rotary positions of queries and keys. Pair i < r / 2 of every head turns by
+ * Rotary positions of queries and keys (row-wise, so the rows S of Eq. (13) can
+ * be turned alone; the paper does not name the positions). Pair i < r / 2 of every head turns by
  * the angle pos * f_i; elements r .. d - 1 of a head pass through:
  *   (a, b) -> m (a cos - b sin, b cos + a sin)
  * with (a, b) = elements (i, i + r/2), or (2i, 2i + 1) when interleaved.
