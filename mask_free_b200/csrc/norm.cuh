@@ -24,25 +24,24 @@ struct NormParams {
   void* y;           // [B, R, D] or null
   uint8_t* q;        // [B * R, D] e4m3 or null
   uint8_t* q_scales;
-  float eps;
+  float eps, inv_D;
   int N, R, D, x_full, h_full, ct;
-  long long rows, rows_pad;  // B * R; with q up to a multiple of 128
+  int rows, rows_pad;  // B * R; with q up to a multiple of 128
+  FastDiv by_R;
 };
 
 // Rows of a tensor for output row `row`; false: a bad index (flagged), the
 // row's outputs are zeros and the stream's row is left as it was. In place
 // (h_full with S) two equal rows would race, so there S has to ascend.
-__device__ __forceinline__ bool norm_rows(const NormParams& p, long long row, bool flag, long long& xr, long long& rr,
-                                          long long& hr) {
+__device__ __forceinline__ bool norm_rows(const NormParams& p, int row, bool flag, int& xr, int& rr, int& hr) {
   xr = rr = hr = row;
   if (p.S == nullptr) return true;
-  const long long b = row / p.R;
-  const int r = static_cast<int>(row - b * p.R);
+  const int b = p.R == 1 ? row : static_cast<int>(p.by_R.div(row)), r = row - b * p.R;
   const int idx = __ldg(p.S + row);
   bool ok = idx >= 0 && idx < p.N;
   if (p.h_full && r > 0 && __ldg(p.S + row - 1) >= idx) ok = false;
   if (!ok && flag) raise_status(1 << 5);
-  const long long full = b * p.N + idx;
+  const int full = b * p.N + idx;  // B N <= INT_MAX
   if (p.x_full) xr = full;
   rr = full;
   if (p.h_full) hr = full;
@@ -86,21 +85,21 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const N
   constexpr int kRowsCta = TPR < 128 ? 128 / TPR : 1, VEC = kMode == kNormOne ? 1 : 8;
   __shared__ float part[TPR < 32 ? 1 : TPR / 32];
   const int t = threadIdx.x % TPR;
-  const long long row = static_cast<long long>(blockIdx.x) * kRowsCta + threadIdx.x / TPR;
+  const int row = static_cast<int>(blockIdx.x * kRowsCta + threadIdx.x / TPR);  // below 2^31
   // rows past the last take part in the shuffles as zeros; those that fill the
   // last scale tile up write their scales, zeros too
   const bool live = row < p.rows;
-  long long xr = 0, rr = 0, hr = 0;
+  int xr = 0, rr = 0, hr = 0;
   const bool ok = live && norm_rows(p, row, t == 0, xr, rr, hr);
-  const T* x = static_cast<const T*>(p.x) + (ok ? xr : 0) * p.D;
-  const T* res = p.res != nullptr ? static_cast<const T*>(p.res) + (ok ? rr : 0) * p.D : nullptr;
-  T* h = p.h != nullptr ? static_cast<T*>(p.h) + (ok ? hr : p.h_full || !live ? 0 : row) * p.D : nullptr;
-  T* y = p.y != nullptr ? static_cast<T*>(p.y) + (live ? row : 0) * p.D : nullptr;
+  const T* x = static_cast<const T*>(p.x) + static_cast<size_t>(ok ? xr : 0) * p.D;
+  const T* res = p.res != nullptr ? static_cast<const T*>(p.res) + static_cast<size_t>(ok ? rr : 0) * p.D : nullptr;
+  T* h = p.h != nullptr ? static_cast<T*>(p.h) + static_cast<size_t>(ok ? hr : p.h_full || !live ? 0 : row) * p.D : nullptr;
+  T* y = p.y != nullptr ? static_cast<T*>(p.y) + static_cast<size_t>(live ? row : 0) * p.D : nullptr;
   const bool h_write = p.h != nullptr && (ok || (live && !p.h_full));
   // first element of unit u (shifted: of the row's first whole unit or before), units
-  const int shift = kMode == kNormShift ? static_cast<int>((row * p.D) & 7) : 0;
+  const int shift = kMode == kNormShift ? static_cast<int>((static_cast<uint32_t>(row) * static_cast<uint32_t>(p.D)) & 7u) : 0;
   const int units = kMode == kNormOne ? p.D : (p.D + shift + 7) / 8;
-  const long long left = kMode == kNormShift ? (p.rows - row) * p.D : 0;  // elements of the tensor from the row's first on
+  const long long left = kMode == kNormShift ? static_cast<long long>(p.rows - row) * p.D : 0;  // elements of the tensor from the row's first on
 
   float v[NV * VEC];
   if constexpr (kMode == kNormOne) {
@@ -174,7 +173,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const N
     for (int i = 0; i < NV; ++i) ss = fmaf(v[i], v[i], ss);
   }
   ss = row_sum<TPR>(ss, part);
-  const float rstd = ok ? 1.f / sqrtf(ss / static_cast<float>(p.D) + p.eps) : 0.f;
+  const float rstd = ok ? 1.f / sqrtf(fmaf(ss, p.inv_D, p.eps)) : 0.f;
 
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const N
           word |= __shfl_xor_sync(0xffffffffu, word, 8);
           if (in && row < p.rows_pad) {
             if (live)
-              *reinterpret_cast<uint2*>(p.q + row * p.D + u * 8) =
+              *reinterpret_cast<uint2*>(p.q + static_cast<size_t>(row) * p.D + u * 8) =
                   e4m3x8(f, inv);
             if ((t & 15) == 0) *reinterpret_cast<uint32_t*>(p.q_scales + mx_scale_at(row, u >> 2, p.ct)) = word;
           }
@@ -252,14 +251,14 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const N
 template <typename T>
 __global__ void __launch_bounds__(512) rms_norm_long_kernel(const NormParams p) {
   __shared__ float part[16];
-  const long long row = blockIdx.x;
-  long long xr, rr, hr;
+  const int row = static_cast<int>(blockIdx.x);
+  int xr, rr, hr;
   const bool ok = norm_rows(p, row, threadIdx.x == 0, xr, rr, hr);
-  const T* x = static_cast<const T*>(p.x) + (ok ? xr : 0) * p.D;
-  const T* res = p.res != nullptr ? static_cast<const T*>(p.res) + (ok ? rr : 0) * p.D : nullptr;
-  T* h = p.h != nullptr ? static_cast<T*>(p.h) + (ok ? hr : p.h_full ? 0 : row) * p.D : nullptr;
+  const T* x = static_cast<const T*>(p.x) + static_cast<size_t>(ok ? xr : 0) * p.D;
+  const T* res = p.res != nullptr ? static_cast<const T*>(p.res) + static_cast<size_t>(ok ? rr : 0) * p.D : nullptr;
+  T* h = p.h != nullptr ? static_cast<T*>(p.h) + static_cast<size_t>(ok ? hr : p.h_full ? 0 : row) * p.D : nullptr;
   const bool h_write = p.h != nullptr && (ok || !p.h_full);
-  T* y = p.y != nullptr ? static_cast<T*>(p.y) + row * p.D : nullptr;
+  T* y = p.y != nullptr ? static_cast<T*>(p.y) + static_cast<size_t>(row) * p.D : nullptr;
   float ss = 0.f;
   if (ok)
     for (int u = threadIdx.x; u < p.D; u += 512) {
@@ -268,7 +267,7 @@ __global__ void __launch_bounds__(512) rms_norm_long_kernel(const NormParams p) 
       ss = fmaf(v, v, ss);
     }
   ss = row_sum<512>(ss, part);
-  const float rstd = ok ? 1.f / sqrtf(ss / static_cast<float>(p.D) + p.eps) : 0.f;
+  const float rstd = ok ? 1.f / sqrtf(fmaf(ss, p.inv_D, p.eps)) : 0.f;
   for (int u = threadIdx.x; u < p.D; u += 512) {
     float v = 0.f;
     if (ok) {

@@ -508,6 +508,12 @@ bool allow_smem(int bytes) {
   return true;
 }
 
+FastDiv fast_div(uint32_t d) {  // d >= 2
+  uint32_t l = 1;
+  while ((1ull << l) < d) ++l;
+  return FastDiv{static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), l - 1};
+}
+
 constexpr int kNormMaxVec = 512 * 8 * 10;  // longest row that rms_norm_kernel holds in registers
 
 template <typename T, int kMode, int NV, int TPR>
@@ -537,7 +543,6 @@ safe_status launch_norm_units(const NormParams& p, int units, cudaStream_t s) {
 
 template <typename T>
 safe_status launch_norm(const NormParams& p, int mode, cudaStream_t s) {
-  if (p.rows_pad > INT_MAX) return SAFE_ERR_UNSUPPORTED;
   if (mode == kNormVec && p.D <= kNormMaxVec) return launch_norm_units<T, kNormVec>(p, p.D / 8, s);
   if (mode == kNormShift && p.D > 64 && p.D <= 20480 - 14) return launch_norm_units<T, kNormShift>(p, (p.D + 14) / 8, s);
   if (p.D <= 8) return norm_launch<T, kNormOne, 2, 4>(p, s);
@@ -589,12 +594,6 @@ safe_status launch_rope(RopeParams& p, bool pairs, bool vec, cudaStream_t s) {
   if (pairs) rope_kernel<T, true><<<grid, 32 * kRopeWarps, smem, s>>>(p);
   else rope_kernel<T, false><<<grid, 32 * kRopeWarps, smem, s>>>(p);
   return launch_status();
-}
-
-FastDiv fast_div(uint32_t d) {  // d >= 2
-  uint32_t l = 1;
-  while ((1ull << l) < d) ++l;
-  return FastDiv{static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), l - 1};
 }
 
 // Calls launch(first row, rows, positions) over slices of whole 128-row groups
@@ -1143,7 +1142,8 @@ safe_status safe_rms_norm(const void* x, int x_full, const void* res, const int3
   if (!aligned_to(q, 16) || !aligned_to(q_scales, 16)) return SAFE_ERR_INVALID_ARG;
   const int R = S != nullptr ? k : N;
   NormParams p{};
-  p.rows = static_cast<long long>(B) * R;
+  p.rows = B * R;  // <= B N <= INT_MAX
+  if (p.rows > INT_MAX - 511) return SAFE_ERR_UNSUPPORTED;  // and the last CTA's rows
   const size_t n_full = static_cast<size_t>(B) * N * D, n_rows = static_cast<size_t>(p.rows) * D;
   // outputs apart from each other and from the inputs; without S, h and y may
   // take the place of x or res (each row is read before it is written)
@@ -1183,6 +1183,8 @@ safe_status safe_rms_norm(const void* x, int x_full, const void* res, const int3
   p.h_full = h_full ? 1 : 0;
   p.ct = q != nullptr ? mx_tiles(D, SAFE_MXFP8) : 0;
   p.rows_pad = q != nullptr ? (p.rows + 127) / 128 * 128 : p.rows;
+  p.inv_D = 1.f / static_cast<float>(D);
+  p.by_R = fast_div(static_cast<uint32_t>(R > 1 ? R : 2));
   switch (dtype) {
     case SAFE_F32: return launch_norm<float>(p, mode, as_stream(stream));
     case SAFE_F16: return launch_norm<__half>(p, mode, as_stream(stream));

@@ -241,8 +241,39 @@ def test_binding_refuses_cpu_tensors():
     _refused(ops.mx_quantize, x, "mxfp8")
 
 
+def test_calls_run_on_the_tensors_device(rec, monkeypatch):
+    # tensors of another device than the current one: the call runs there, on
+    # that device's current stream
+    entered = []
+
+    class Device:
+        def __init__(self, i):
+            self.i = i
+
+        def __enter__(self):
+            entered.append(self.i)
+
+        def __exit__(self, *a):
+            entered.append(-1)
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(ops, "_raw_stream", lambda i: 100 + i)
+    ops._run("safe_mx_dequantize", torch.device("cuda", 0), 1)
+    assert entered == [] and rec.calls[-1][1] == (1, 100)
+    ops._run("safe_mx_dequantize", torch.device("cuda", 1), 1)
+    assert entered == [1, -1] and rec.calls[-1][1] == (1, 101)
+    assert ops._on(torch.device("cuda", 2), lambda v: v, 5) == 5 and entered[2:] == [2, -1]
+
+
+def test_checked_operands_cannot_be_exchanged(rec):
+    m, tab = mx(4, 64), table(32)
+    for obj, name in ((m, "data"), (m, "scales"), (m, "scale"), (tab, "freq"), (tab, "sections")):
+        with pytest.raises(AttributeError):
+            setattr(obj, name, getattr(obj, name))
+
+
 # ---------------------------------------------------------------- the library
-P = ctypes.c_void_p(0x100000)
 
 
 def at(n):
