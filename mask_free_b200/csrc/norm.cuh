@@ -76,13 +76,14 @@ enum : int { kNormVec, kNormShift, kNormOne };
 
 // TPR threads take a row, each NV units of 8 elements (one in kNormOne), and keep
 // it in registers between the sum and the output: one read of x and res. Bound
-// by memory. Few registers for each thread and many rows at once keep more
-// loads in flight than long rows in one warp: D = 2304 on 128 threads with 3
-// units each takes 47 us for 12800 rows (8-bit output), on a warp with 10
-// units 53.
+// by memory, and with the 8-bit output by issue. Few registers for each thread
+// and many rows at once keep more loads in flight than long rows in one warp,
+// and idle threads cost issue slots: 12800 rows of 2304 to 8 bits take 43 us
+// on 96 threads with 3 units each, 47 - 49 on 128 (a quarter of the units past
+// the end), 53 on a warp with 10 units.
 template <typename T, int kMode, int NV, int TPR>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const NormParams p) {
-  constexpr int kRowsCta = TPR < 128 ? 128 / TPR : 1, VEC = kMode == kNormOne ? 1 : 8;
+__global__ void __launch_bounds__(TPR <= 32 ? 128 : TPR) rms_norm_kernel(const NormParams p) {
+  constexpr int kRowsCta = TPR <= 32 ? 128 / TPR : 1, VEC = kMode == kNormOne ? 1 : 8;
   __shared__ float part[TPR < 32 ? 1 : TPR / 32];
   const int t = threadIdx.x % TPR;
   const int row = static_cast<int>(blockIdx.x * kRowsCta + threadIdx.x / TPR);  // below 2^31

@@ -518,21 +518,24 @@ constexpr int kNormMaxVec = 512 * 8 * 10;  // longest row that rms_norm_kernel h
 
 template <typename T, int kMode, int NV, int TPR>
 safe_status norm_launch(const NormParams& p, cudaStream_t s) {
-  constexpr int rows_cta = TPR < 128 ? 128 / TPR : 1;
+  constexpr int rows_cta = TPR <= 32 ? 128 / TPR : 1;
   rms_norm_kernel<T, kMode, NV, TPR>
-      <<<static_cast<unsigned>((p.rows_pad + rows_cta - 1) / rows_cta), TPR < 128 ? 128 : TPR, 0, s>>>(p);
+      <<<static_cast<unsigned>((p.rows_pad + rows_cta - 1) / rows_cta), TPR <= 32 ? 128 : TPR, 0, s>>>(p);
   return launch_status();
 }
 
 // The fewest threads that hold a row in a few units each: part of a warp for
-// short rows (51200 rows of 128: 14 us, with a warp for each 25), a warp, 128 threads, 512.
+// short rows (51200 rows of 128: 14 us, with a warp for each 25), a warp, 96 or 128 threads,
+// 512.
 template <typename T, int kMode>
 safe_status launch_norm_units(const NormParams& p, int units, cudaStream_t s) {
   if (kMode == kNormVec && units <= 8 && p.q == nullptr) return norm_launch<T, kNormVec, 2, 4>(p, s);
   if (units <= 32) return norm_launch<T, kMode, 2, 16>(p, s);
   if (units <= 64) return norm_launch<T, kMode, 2, 32>(p, s);
   if (units <= 128) return norm_launch<T, kMode, 4, 32>(p, s);
+  if (units <= 192) return norm_launch<T, kMode, 2, 96>(p, s);
   if (units <= 256) return norm_launch<T, kMode, 2, 128>(p, s);
+  if (units <= 288) return norm_launch<T, kMode, 3, 96>(p, s);
   if (units <= 384) return norm_launch<T, kMode, 3, 128>(p, s);
   if (units <= 512) return norm_launch<T, kMode, 4, 128>(p, s);
   if (units <= 896) return norm_launch<T, kMode, 7, 128>(p, s);
