@@ -14,6 +14,7 @@ import math
 import os
 from typing import Optional, Sequence, Tuple
 
+import numpy as np
 import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsafe_attn.so")
@@ -800,9 +801,9 @@ def rope_table(r: int, base: float = 10000.0, sections: Optional[Sequence[int]] 
     rope_frequencies. sections share the r / 2 pairs out over up to three
     position axes (e.g. rows and columns of the latent grid)."""
     f, m = rope_frequencies(r, base, sections, **scaling)
-    turns = [int(math.ldexp(v / (2 * math.pi), 64)) & (2 ** 64 - 1) for v in f]
-    freq = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
-    return RopeTable(freq, [r // 2] if sections is None else sections, m)
+    turns = np.array(f) / (2 * math.pi)
+    fixed = np.ldexp(turns - np.floor(turns), 64).astype(np.uint64).view(np.int64)  # exact: below 2^64
+    return RopeTable(torch.from_numpy(fixed).to(device), [r // 2] if sections is None else sections, m)
 
 
 def _heads(t, name: str, dtype, B, R, d, dev):

@@ -82,6 +82,14 @@ def test_frequencies():
         _refused(ops.rope_frequencies, **bad)
 
 
+def test_rope_table_is_the_frequencies_in_turns(rec):
+    f, m = ops.rope_frequencies(64, kind="yarn", factor=4.0, original_len=1024)
+    tab = ops.rope_table(64, device="cpu", kind="yarn", factor=4.0, original_len=1024)
+    got = [int(v) % 2 ** 64 / 2.0 ** 64 for v in tab.freq]
+    np.testing.assert_allclose(got, np.array(f) / (2 * math.pi), rtol=2.0 ** -50)
+    assert tab.m == m and tab.sections == (32,) and tab.r == 64
+
+
 def test_microscaled_pins():
     # e4m3 table: largest 448, one 56; torch's own conversion agrees on every code
     assert len(O.E4M3) == 127 and O.E4M3[126] == 448.0 and O.E4M3[56] == 1.0
