@@ -802,7 +802,7 @@ def rope_table(r: int, base: float = 10000.0, sections: Optional[Sequence[int]] 
     position axes (e.g. rows and columns of the latent grid)."""
     f, m = rope_frequencies(r, base, sections, **scaling)
     turns = np.array(f) / (2 * math.pi)
-    fixed = np.ldexp(turns - np.floor(turns), 64).astype(np.uint64).view(np.int64)  # exact: below 2^64
+    fixed = np.rint(np.ldexp(turns - np.floor(turns), 64)).astype(np.uint64).view(np.int64)  # at most 2^64 - 2^11
     return RopeTable(torch.from_numpy(fixed).to(device), [r // 2] if sections is None else sections, m)
 
 
