@@ -182,6 +182,24 @@ def test_norm_updates_the_stream_in_place():
     assert ops.device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", [bf16, f32])
+@pytest.mark.parametrize("D", [65, 131, 1021, 2303, 4100])
+def test_norm_of_odd_widths_in_place_and_beside_nan(dtype, D):
+    # rows that share 16-byte units with their neighbours: in place the same
+    # bits as apart, and a NaN or an infinity stays in its row
+    x, r, w = randn((2, 37, D), 1, dtype).to(DEV), randn((2, 37, D), 2, dtype).to(DEV), randn((D,), 3).to(DEV)
+    y0, h0 = ops.rms_norm(x, w, r)
+    xs, rs = x.clone(), r.clone()
+    y1, h1 = ops.rms_norm(xs, w, rs, update=True, out=xs)
+    assert y1 is xs and h1 is rs and torch.equal(y1, y0) and torch.equal(h1, h0)
+    x[0, 5, D - 1], x[1, 0, 0], x[1, 36, D - 1] = float("nan"), float("inf"), float("nan")
+    y2, h2 = ops.rms_norm(x, w, r)
+    clean = torch.ones((2, 37), dtype=torch.bool, device=DEV)
+    clean[0, 5] = clean[1, 0] = clean[1, 36] = False
+    assert torch.equal(y2[clean], y0[clean]) and torch.equal(h2[clean], h0[clean])
+    assert y2[0, 5].isnan().all() and y2[1, 36].isnan().all() and ops.device_status() == 0
+
+
 @pytest.mark.parametrize("D", [64, 2304])
 def test_norm_with_both_outputs(D):
     # the C entry point writes y and its 8-bit form in one call
