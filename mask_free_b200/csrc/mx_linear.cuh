@@ -190,18 +190,25 @@ __device__ __forceinline__ uint64_t gelu_tanh_2(uint64_t x) {
   return f2_mul(x, f2_pack(rcp_approx(a), rcp_approx(b)));
 }
 
-// act(alpha v + bias) of a row's next 64 columns (of which `left` exist),
-// rounded to bf16, to memory: stores of 32 bytes (whole sectors) where rows are
-// so aligned, else of 16.
+// act(alpha v + bias) of a row's next 64 columns (of which `left` exist), rounded
+// to bf16, to memory: stores of 32 bytes (whole sectors) where rows are so
+// aligned, else of 16. Every lane reads all 64 biases from shared memory, in
+// single words: vectors that all lanes read at once took six passes each, 1 - 3 %
+// of a call.
 template <bool kGelu>
-__device__ __forceinline__ void mx_store_row(const uint32_t* v, float alpha, const float4* bias, __nv_bfloat16* y, int left,
+__device__ __forceinline__ void mx_store_row(const uint32_t* v, float alpha, uint32_t bias, __nv_bfloat16* y, int left,
                                              int wide) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {  // 16 columns
     uint32_t w[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float4 b = bias[4 * c + k];
+      const uint32_t at = bias + 4 * (16 * c + 4 * k);
+      float4 b;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(b.x) : "r"(at));
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(b.y) : "r"(at + 4));
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(b.z) : "r"(at + 8));
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(b.w) : "r"(at + 12));
       const uint64_t al = f2_pack(alpha, alpha);
       uint64_t f0 = f2_fma(f2_pack(__uint_as_float(v[16 * c + 4 * k]), __uint_as_float(v[16 * c + 4 * k + 1])), al, f2_pack(b.x, b.y));
       uint64_t f1 = f2_fma(f2_pack(__uint_as_float(v[16 * c + 4 * k + 2]), __uint_as_float(v[16 * c + 4 * k + 3])), al, f2_pack(b.z, b.w));
@@ -440,8 +447,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     const int q = warp & 3, e = (warp - 4) >> 2;
     const uint32_t lane_addr = tbase + (static_cast<uint32_t>(q * 32) << 16) + 64 * e;
     const uint32_t acce0 = cluster_addr(acc_empty, 0), she0 = cluster_addr(sh_empty, 0);
-    const float4* bias = reinterpret_cast<const float4*>(sBias + 64 * (warp - 4));
     float2* bias2 = reinterpret_cast<float2*>(sBias + 64 * (warp - 4));
+    const uint32_t bias = smem_u32(bias2);
     auto tile = [&](int i) {  // of unit i (past the last: the first's)
       const int u = i < n_local ? pair + i * n_pairs : pair;
       return u < p.whole ? u : p.whole + p.piece_tile[u - p.whole];
