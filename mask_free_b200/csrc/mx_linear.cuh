@@ -26,8 +26,8 @@
 //
 // What bounds it: a stage is 34 - 38 KB into shared memory and as much out of
 // it for 512 cycles of MMA, and 1000 W. A call by itself (PFLOP/s; 51200 rows at
-// d_in = 2304, 12800 at 9216, d_out 6912): nvfp4 5.1 and 6.2, mxfp4 5.3 and 6.5,
-// mxfp8 3.05 and 2.85, with clocks down to 1.45 and 1.25 GHz; calls back to
+// d_in = 2304, 12800 at 9216, d_out 6912): nvfp4 5.2 and 6.2, mxfp4 5.6 and 6.6,
+// mxfp8 3.1 and 2.9, with clocks down to 1.45 and 1.25 GHz; calls back to
 // back, when power sets the clock: nvfp4 3.9 and 4.9, mxfp8 2.3 and 2.25.
 // Measured on the way (nvfp4, d_in 2304 / 9216): tiles of 192 columns with
 // accumulators apart 4.2 / 4.9; accumulators that overlap without the split
@@ -174,7 +174,9 @@ __host__ __device__ constexpr int mx_stage_tiles(int fmt) { return fmt == kMxFp8
 __host__ __device__ constexpr int mx_stage_bytes(int fmt) { return kMxABytes + kMxBBytes + 3 * 512 * mx_stage_tiles(fmt); }
 // As many stages as fit (5 of nvfp4, 6 of the others).
 __host__ __device__ constexpr int mx_stages(int fmt) { return (227 * 1024 - 1024 - 16 * 256 - 256) / mx_stage_bytes(fmt); }
-__host__ __device__ constexpr int mx_linear_smem(int fmt) { return 1024 + mx_stages(fmt) * mx_stage_bytes(fmt) + 16 * 256 + 256; }
+__host__ __device__ constexpr int mx_linear_smem(int fmt) {
+  return 1024 + mx_stages(fmt) * mx_stage_bytes(fmt) + 16 * 256 + 256;
+}
 
 // GELU in its tanh form of two values: x / (1 + 2^t), t = x (c1 + c2 x^2) with
 // c1 = -2 sqrt(2 / pi) / ln 2 and c2 = 0.044715 c1 (see gelu_tanh_f), in packed
@@ -210,8 +212,9 @@ __device__ __forceinline__ void mx_store_row(const uint32_t* v, float alpha, uin
       asm volatile("ld.shared.f32 %0, [%1];" : "=f"(b.z) : "r"(at + 8));
       asm volatile("ld.shared.f32 %0, [%1];" : "=f"(b.w) : "r"(at + 12));
       const uint64_t al = f2_pack(alpha, alpha);
-      uint64_t f0 = f2_fma(f2_pack(__uint_as_float(v[16 * c + 4 * k]), __uint_as_float(v[16 * c + 4 * k + 1])), al, f2_pack(b.x, b.y));
-      uint64_t f1 = f2_fma(f2_pack(__uint_as_float(v[16 * c + 4 * k + 2]), __uint_as_float(v[16 * c + 4 * k + 3])), al, f2_pack(b.z, b.w));
+      const uint32_t* vk = v + 16 * c + 4 * k;
+      uint64_t f0 = f2_fma(f2_pack(__uint_as_float(vk[0]), __uint_as_float(vk[1])), al, f2_pack(b.x, b.y));
+      uint64_t f1 = f2_fma(f2_pack(__uint_as_float(vk[2]), __uint_as_float(vk[3])), al, f2_pack(b.z, b.w));
       if constexpr (kGelu) {
         f0 = gelu_tanh_2(f0);
         f1 = gelu_tanh_2(f1);
@@ -353,8 +356,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     // descriptors: constant high words, and low words (the address in 16s,
     // below 2^14 everywhere) that move with the stage
     constexpr uint64_t kMat = 0xFFFFFFFF00000000ull;
-    const uint64_t dA = make_sdesc(smem_u32(sA), 16, 1024, kSwizzle128B), dB = make_sdesc(smem_u32(sB), 16, 1024, kSwizzle128B);
-    const uint64_t dSA = make_sdesc(smem_u32(sSA), 0, 128, kSwizzleNone), dSB = make_sdesc(smem_u32(sSB), 0, 128, kSwizzleNone);
+    const uint64_t dA = make_sdesc(smem_u32(sA), 16, 1024, kSwizzle128B);
+    const uint64_t dB = make_sdesc(smem_u32(sB), 16, 1024, kSwizzle128B);
+    const uint64_t dSA = make_sdesc(smem_u32(sSA), 0, 128, kSwizzleNone);
+    const uint64_t dSB = make_sdesc(smem_u32(sSB), 0, 128, kSwizzleNone);
     auto at = [&](uint64_t d, uint32_t lo) { return (d & kMat) | lo; };
     const int last_steps = (p.row_bytes - 128 * (nk - 1) + 31) / 32;  // 32-byte steps of the last stage
     int s = 0;
@@ -379,8 +384,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t la = static_cast<uint32_t>(dA) + s * (kMxABytes >> 4), lb = static_cast<uint32_t>(dB) + s * (kMxBBytes >> 4);
-        const uint32_t lsa = static_cast<uint32_t>(dSA) + s * (kSfA >> 4), lsb = static_cast<uint32_t>(dSB) + s * (kSfB >> 4);
+        const uint32_t la = static_cast<uint32_t>(dA) + s * (kMxABytes >> 4);
+        const uint32_t lb = static_cast<uint32_t>(dB) + s * (kMxBBytes >> 4);
+        const uint32_t lsa = static_cast<uint32_t>(dSA) + s * (kSfA >> 4);
+        const uint32_t lsb = static_cast<uint32_t>(dSB) + s * (kSfB >> 4);
 #pragma unroll
         for (int j = 0; j < KT; ++j) {
           tmem_copy_scales_pair_if(leader, sfa + 4 * j, at(dSA, lsa + 32 * j));
@@ -393,8 +400,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           // scale tile and byte of step kk
           constexpr int per = 4 / KT;  // steps that share a tile
           const int j = kk / per, id = kFmt == kMxFp8 ? kk : kFmt == kMxFp4 ? 2 * (kk & 1) : 0;
-          umma_pair_mx_if<kFmt>(kk < steps ? leader : 0u, d, at(dA, la + 2 * kk), at(dB, b + 2 * kk), make_idesc_mx(kFmt, 256, N, id),
-                                sfa + 4 * j, sf + 8 * j, kk != 0 ? 1u : acc);
+          umma_pair_mx_if<kFmt>(kk < steps ? leader : 0u, d, at(dA, la + 2 * kk), at(dB, b + 2 * kk),
+                                make_idesc_mx(kFmt, 256, N, id), sfa + 4 * j, sf + 8 * j, kk != 0 ? 1u : acc);
         };
         auto all = [&] {
 #pragma unroll
@@ -468,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       bias2[lane] = next;
       next = load_bias(i + 1);
       const bool sh = e == (a ? 0 : 3);
-      if (!(sh ? warp_wait_short(sh_full, i & 1, &abort_flag) : warp_wait_short(&acc_full[a], (i >> 1) & 1, &abort_flag))) break;
+      if (!warp_wait_short(sh ? sh_full : &acc_full[a], sh ? i & 1 : (i >> 1) & 1, &abort_flag)) break;
       tc_fence_after();
       uint32_t v[64];
       tmem_ld32(lane_addr + 192 * a, v);

@@ -262,8 +262,8 @@ __device__ __forceinline__ float e2m1_border(uint32_t c) {
 }
 
 // Eight elements of an nvfp4 block with scale value s (inv ~ 1 / (s g) within
-// 3 2^-24; the product with v and that with 1 -+ 2^-21 add 2^-24 each): nearest e2m1 of v / (s g), exactly, by the same two conversions;
-// where they differ, the element's border's product border * s (7 bits) decides
+// 3 2^-24; the product with v and that with 1 -+ 2^-21 add 2^-24 each):
+// nearest e2m1 of v / (s g), exactly, by the same two conversions; where they differ, the element's border's product border * s (7 bits) decides
 // by the sign of one fma, and a tie goes to the even code. (Ties are common
 // where g is a short number: bf16 inputs have 8 bits. So the loop takes only
 // the elements that differ; a pass over all eight cost 30 us at 51200 x 2304.)
@@ -406,13 +406,15 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const MxQuantParams p)
     words[i] = word;
     if (live && in && row < p.rows) {
       if constexpr (kFmt == kMxFp8)
-        *reinterpret_cast<uint4*>(p.data + static_cast<size_t>(row) * p.D + unit * 16) = make_uint4(out[0], out[1], out[2], out[3]);
+        *reinterpret_cast<uint4*>(p.data + static_cast<size_t>(row) * p.D + unit * 16) =
+            make_uint4(out[0], out[1], out[2], out[3]);
       else
         *reinterpret_cast<uint2*>(p.data + static_cast<size_t>(row) * (p.D / 2) + unit * 8) = make_uint2(out[0], out[1]);
     }
   }
   if (live && (threadIdx.x & (kLanes - 1)) == 0)
-    *reinterpret_cast<uint4*>(p.scales + mx_scale_at(r0, unit / (kLanes / 4), p.ct)) = make_uint4(words[0], words[1], words[2], words[3]);
+    *reinterpret_cast<uint4*>(p.scales + mx_scale_at(r0, unit / (kLanes / 4), p.ct)) =
+        make_uint4(words[0], words[1], words[2], words[3]);
 }
 
 // ---------------------------------------------------------------- decoding

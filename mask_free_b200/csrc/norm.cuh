@@ -98,9 +98,10 @@ __global__ void __launch_bounds__(TPR <= 32 ? 128 : TPR) rms_norm_kernel(const N
   T* y = p.y != nullptr ? static_cast<T*>(p.y) + static_cast<size_t>(live ? row : 0) * p.D : nullptr;
   const bool h_write = p.h != nullptr && (ok || (live && !p.h_full));
   // first element of unit u (shifted: of the row's first whole unit or before), units
-  const int shift = kMode == kNormShift ? static_cast<int>((static_cast<uint32_t>(row) * static_cast<uint32_t>(p.D)) & 7u) : 0;
+  const int shift = kMode == kNormShift ? (row & 7) * (p.D & 7) & 7 : 0;
   const int units = kMode == kNormOne ? p.D : (p.D + shift + 7) / 8;
-  const long long left = kMode == kNormShift ? static_cast<long long>(p.rows - row) * p.D : 0;  // elements of the tensor from the row's first on
+  // elements of the tensor from the row's first on
+  const long long left = kMode == kNormShift ? static_cast<long long>(p.rows - row) * p.D : 0;
 
   float v[NV * VEC];
   if constexpr (kMode == kNormOne) {
@@ -142,7 +143,8 @@ __global__ void __launch_bounds__(TPR <= 32 ? 128 : TPR) rms_norm_kernel(const N
         b[i].get(f);
 #pragma unroll
         for (int e = 0; e < 8; e += 2)
-          f2_unpack(f2_add(f2_pack(v[8 * i + e], v[8 * i + e + 1]), f2_pack(f[e], f[e + 1])), v[8 * i + e], v[8 * i + e + 1]);
+          f2_unpack(f2_add(f2_pack(v[8 * i + e], v[8 * i + e + 1]), f2_pack(f[e], f[e + 1])), v[8 * i + e],
+                    v[8 * i + e + 1]);
       }
     } else {
 #pragma unroll

@@ -61,7 +61,9 @@ __device__ __forceinline__ float2 rope_rotation(const RopeParams& p, int i, long
   sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
   return make_float2(c * p.m, s * p.m);
 }
-__device__ __forceinline__ int rope_axis(const RopeParams& p, int i) { return i < p.sec0 ? 0 : i < p.sec0 + p.sec1 ? 1 : 2; }
+__device__ __forceinline__ int rope_axis(const RopeParams& p, int i) {
+  return i < p.sec0 ? 0 : i < p.sec0 + p.sec1 ? 1 : 2;
+}
 
 // Turns 8 pairs: a and v hold pairs (e, e) (halves) or 4 neighbouring pairs each.
 template <bool kPairs>
@@ -86,7 +88,8 @@ __device__ __forceinline__ void rope_turn(float* a, float* v, const float2* w) {
 }
 
 // The r / 2 rotations of a token (m cos, m sin), by `n` threads.
-__device__ __forceinline__ void rope_rotations(const RopeParams& p, const int32_t* pos, int token, int t, int n, float2* cs) {
+__device__ __forceinline__ void rope_rotations(const RopeParams& p, const int32_t* pos, int token, int t, int n,
+                                               float2* cs) {
   for (int i = t; i < p.r / 2; i += n) cs[i] = rope_rotation(p, i, pos != nullptr ? __ldg(pos + rope_axis(p, i)) : token);
 }
 

@@ -1146,7 +1146,8 @@ safe_status safe_rms_norm(const void* x, int x_full, const void* res, const int3
   const int R = S != nullptr ? k : N;
   NormParams p{};
   p.rows = B * R;  // <= B N <= INT_MAX
-  if (p.rows > INT_MAX - 511) return SAFE_ERR_UNSUPPORTED;  // and the last CTA's rows
+  // room for the counters past the last row and element
+  if (p.rows > INT_MAX - 511 || D > INT_MAX - 511) return SAFE_ERR_UNSUPPORTED;
   const size_t n_full = static_cast<size_t>(B) * N * D, n_rows = static_cast<size_t>(p.rows) * D;
   // outputs apart from each other and from the inputs; without S, h and y may
   // take the place of x or res (each row is read before it is written)
@@ -1331,7 +1332,7 @@ safe_status safe_mx_dequantize(const void* data, const void* scales, int fmt, fl
 
 size_t safe_mx_linear_workspace_bytes(int64_t rows, int d_in, int d_out, int fmt) {
   if (fmt < SAFE_MXFP8 || fmt > SAFE_NVFP4 || rows < 1 || rows > kMxMaxRows || d_in < 64 || d_in % 32 != 0 || d_out < 8 ||
-      d_out % 8 != 0)
+      d_out > kMxMaxRows || d_out % 8 != 0)
     return 0;
   return mx_linear_plan(rows, d_out, fmt == SAFE_MXFP8 ? d_in : d_in / 2, mx_linear_pairs(fmt), true).part_bytes;
 }
@@ -1344,7 +1345,7 @@ safe_status safe_mx_linear(const void* X, const void* X_scales, const void* Wt, 
     return SAFE_ERR_INVALID_ARG;
   if (fmt < SAFE_MXFP8 || fmt > SAFE_NVFP4 || !std::isnormal(alpha) || (act != 0 && act != 1)) return SAFE_ERR_INVALID_ARG;
   if (rows < 1 || rows > INT_MAX || d_in < 64 || d_in % 32 != 0 || d_out < 8 || d_out % 8 != 0) return SAFE_ERR_INVALID_ARG;
-  if (rows > kMxMaxRows) return SAFE_ERR_UNSUPPORTED;
+  if (rows > kMxMaxRows || d_out > kMxMaxRows) return SAFE_ERR_UNSUPPORTED;
   const int row_bytes = fmt == SAFE_MXFP8 ? d_in : d_in / 2;
   const size_t yb = static_cast<size_t>(rows) * d_out * 2;
   if (overlap(Y, yb, X, static_cast<size_t>(rows) * row_bytes) ||

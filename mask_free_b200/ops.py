@@ -560,7 +560,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _check_tensor(t, name: str, dtype, shape, dev):
     """_need for a known shape on a known device, quick when all is well."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
         _need(t, name, dtype, len(shape), shape, dev)
 
 
@@ -741,7 +742,8 @@ class RopeTable:
         _need(freq, "freq", torch.int64, 1)
         self._sections = tuple(int(n) for n in sections)
         self._r = 2 * freq.shape[0]
-        if not 1 <= len(self._sections) <= 3 or min(self._sections) < 0 or 2 * sum(self._sections) != self._r or self._r < 2:
+        n = self._sections
+        if not 1 <= len(n) <= 3 or min(n) < 0 or 2 * sum(n) != self._r or self._r < 2:
             raise ValueError(f"sections must be 1 to 3 counts that share out {self._r // 2} pairs, got {self._sections}")
         if not math.isfinite(m):
             raise ValueError(f"m must be finite, got {m}")
@@ -892,8 +894,8 @@ def rope(q, k, table: RopeTable, pos=None, S=None, interleaved=False, inplace=Fa
             n, oks = _heads(ok, "out[1]", dtype, B, R, d, dev)
             if n != Hk:
                 raise ValueError(f"out[1] must have {Hk} heads, got {n}")
-    _run("safe_rope", dev, q.data_ptr(), qs, oq.data_ptr(), oqs, H, kp, ks, None if k is None else ok.data_ptr(), oks, Hk, dt,
-         table._freq_ptr, table._counts, axes, pp, batched, sp, B, N, R, d, r, 1 if interleaved else 0, table._m)
+    _run("safe_rope", dev, q.data_ptr(), qs, oq.data_ptr(), oqs, H, kp, ks, None if k is None else ok.data_ptr(), oks, Hk,
+         dt, table._freq_ptr, table._counts, axes, pp, batched, sp, B, N, R, d, r, 1 if interleaved else 0, table._m)
     return oq, ok
 
 
@@ -933,7 +935,8 @@ def mx_quantize(x, fmt: str, S=None, scale: float = 1.0, out=None) -> MxTensor:
             raise ValueError("S needs x of 3 dims")
         R = k = _rows_of(S, B, N, dev)
     m = _mx_out(out, (B, R) if nd == 3 else (N,), D, fmt, g, x)
-    _run("safe_mx_quantize", dev, x.data_ptr(), dt, _ptr(S), k, code, g, m._data.data_ptr(), m._scales.data_ptr(), B, N, D)
+    _run("safe_mx_quantize", dev, x.data_ptr(), dt, _ptr(S), k, code, g, m._data.data_ptr(), m._scales.data_ptr(), B, N,
+         D)
     return m
 
 
@@ -945,8 +948,8 @@ def mx_dequantize(m: MxTensor, dtype=torch.bfloat16, out=None):
         raise ValueError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
     data, D = m._data, m._D
     out = _out_like(out, "out", m._scales, dtype, (*data.shape[:-1], D))
-    _run("safe_mx_dequantize", data.device, data.data_ptr(), m._scales.data_ptr(), _FORMATS[m._fmt], m._scale, out.data_ptr(),
-         _FLOATS[dtype], m._rows, D)
+    _run("safe_mx_dequantize", data.device, data.data_ptr(), m._scales.data_ptr(), _FORMATS[m._fmt], m._scale,
+         out.data_ptr(), _FLOATS[dtype], m._rows, D)
     return out
 
 

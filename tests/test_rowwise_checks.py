@@ -312,6 +312,7 @@ def test_rms_norm_validates_on_host(lib):
     assert call(q=at(6), qs=at(7), D=40) == 1                         # 8 bits: multiples of 32
     assert call(q=at(6), qs=at(7), x=ctypes.c_void_p(0x100002)) == 1  # and 16-byte alignment
     assert call(q=at(6), qs=at(7), D=40992) == 2
+    assert call(N=1, D=2 ** 31 - 1, x=ctypes.c_void_p(1 << 40), res=None, w=None, h=None) == 2  # counters would wrap
     assert call(x=ctypes.c_void_p(0x100001)) == 1 and call(S=ctypes.c_void_p(0x9000002), k=4) == 1
     assert call(y=ctypes.c_void_p(0x100000 + 64)) == 1                # output overlaps an input in part
     assert call(y=at(3)) == 1                                         # outputs overlap
@@ -373,6 +374,9 @@ def test_microscaled_entry_points_validate_on_host(lib):
     assert lin(fmt=3) == 1 and lin(a=float("nan")) == 1 and lin(a=0.0) == 1 and lin(act=2) == 1
     assert lin(rows=0) == 1 and lin(rows=2 ** 31) == 1 and lin(i=32) == 1 and lin(i=80) == 1 and lin(o=12) == 1 and lin(o=0) == 1
     assert lin(bias=ctypes.c_void_p(0x100002)) == 1 and lin(Y=at(0)) == 1 and lin(Y=at(3)) == 1
+    far = [ctypes.c_void_p((i + 1) << 44) for i in range(5)]
+    huge = dict(X=far[0], Xs=far[1], W=far[2], Ws=far[3], Y=far[4])
+    assert lin(**huge, rows=2 ** 31 - 8) == 2 and lin(**huge, o=2 ** 31 - 8) == 2 and lin(**huge, rows=2 ** 31 - 8, o=2 ** 31 - 8) == 2
     # the split of the last wave's tiles (9 of 74 pairs, 72 stages): its workspace, apart from the rest
     big = dict(fmt=0, rows=200, i=9216, o=2304)
     n = lib.safe_mx_linear_workspace_bytes(200, 9216, 2304, 0)
