@@ -340,6 +340,7 @@ struct MxQuantParams {
 // its place, took 72, 70 and 82 us.
 template <typename T, int kFmt>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(const MxQuantParams p) {
+  pdl_launch_dependents();  // a dependent layer may set up meanwhile
   const uint32_t t = blockIdx.x * 256 + threadIdx.x;
   // the grid's last positions past the end repeat the last one, without stores
   const bool live = t < p.threads;

@@ -728,11 +728,24 @@ safe_status launch_mx_linear(MxLinearParams& p, const void* X, const void* Xs, c
     return SAFE_ERR_CUDA;
   if (!allow_smem<mx_linear_pair_kernel<kFmt>>(smem)) return SAFE_ERR_CUDA;
   const int pairs = p.units < plan.pairs ? p.units : plan.pairs;
-  mx_linear_pair_kernel<kFmt><<<2 * pairs, kMxThreads, smem, s>>>(p);
-  if (launch_status() != SAFE_OK) return SAFE_ERR_CUDA;
+  // both launches are programmatic dependents of what precedes them in the stream
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(kMxThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, mx_linear_pair_kernel<kFmt>, p) != cudaSuccess) return SAFE_ERR_CUDA;
   if (plan.rest > 0) {
-    MxMergeParams m{p.part, p.bias, p.Y, p.alpha, p.M, p.d_out, p.act, p.n_tiles, p.whole, plan.split};
-    mx_linear_merge_kernel<<<32 * plan.rest, 256, 0, s>>>(m);
+    const MxMergeParams m{p.part, p.bias, p.Y, p.alpha, p.M, p.d_out, p.act, p.n_tiles, p.whole, plan.split};
+    cfg.gridDim = dim3(static_cast<unsigned>(32 * plan.rest));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    if (cudaLaunchKernelEx(&cfg, mx_linear_merge_kernel, m) != cudaSuccess) return SAFE_ERR_CUDA;
   }
   return launch_status();
 }

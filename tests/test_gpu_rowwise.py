@@ -734,6 +734,50 @@ def test_streams_and_graphs(fmt, k):
     assert ops.device_status() == 0
 
 
+@pytest.mark.parametrize("rows_,d,hidden", [(16, 256, 512), (700, 512, 2304), (4096, 2304, 6912)])
+def test_layers_that_write_what_the_one_before_reads(rows_, d, hidden):
+    # one set of buffers, taken in turn by launches that overlap at their ends; the
+    # last size splits its last wave. Against the same calls one at a time.
+    up = ops.mx_quantize((randn((hidden, d), 1) / math.sqrt(d)).to(DEV), "mxfp8")
+    down = ops.mx_quantize((randn((d, hidden), 2) / math.sqrt(hidden)).to(DEV), "mxfp8")
+    first = randn((rows_, d), 3, bf16).to(DEV)
+    x, h, bias = torch.empty_like(first), torch.empty((rows_, hidden), dtype=bf16, device=DEV), torch.empty(d, device=DEV)
+    nbytes = ops.mx_linear_workspace_bytes(rows_, hidden, d, "mxfp8")
+    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=DEV)
+    X = ops.mx_quantize(first, "mxfp8")
+    H = ops.mx_quantize(torch.zeros_like(h), "mxfp8")
+
+    def run(wait):
+        x.copy_(first)
+        bias.zero_()
+        for i in range(4):
+            ops.mx_quantize(x, "mxfp8", out=X)
+            wait()
+            ops.mx_linear(X, up, act="gelu_tanh", out=h)
+            wait()
+            ops.mx_quantize(h, "mxfp8", out=H)
+            wait()
+            bias.add_(0.25)
+            ops.mx_linear(H, down, bias, out=x, ws=ws)
+            wait()
+            ops.mx_linear(H, down, bias, out=x, ws=ws)  # the same again, behind its own kernels
+            wait()
+        return x.clone()
+
+    want = run(torch.cuda.synchronize)
+    assert want.isfinite().all()
+    for _ in range(5):
+        assert torch.equal(run(lambda: None), want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = run(lambda: None)
+    for _ in range(3):
+        y.zero_()
+        g.replay()
+        assert torch.equal(y, want)
+    assert ops.device_status() == 0
+
+
 def test_first_calls_inside_a_capture():
     # a process whose first calls are captured: nothing in them needs a stream
     code = """
