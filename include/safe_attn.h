@@ -366,8 +366,9 @@ safe_status safe_gather_linear(const void* X, const int32_t* S, int k, const voi
  *  w      device fp32 [D] or NULL (ones).
  *  h      device [B, R, D] (written) or NULL. h_full = 1 (with S, h == res):
  *         the rows S of the stream are updated in place and every other row
- *         is left as it is; S must then be strictly ascending (a row out of
- *         order is flagged, leaves the stream as it is and its y is zero).
+ *         is left as it is; S must then be strictly ascending: a row whose
+ *         index does not lie above every earlier one of its sample is flagged,
+ *         leaves the stream as it is, and its y and q are zeros.
  *  y      device [B, R, D] (written) or NULL.
  *  q, q_scales  device, 16-byte aligned: y as SAFE_MXFP8 matrix of B * R rows
  *         (layout and sizes: safe_mx_quantize), quantised from the fp32 y

@@ -516,12 +516,26 @@ FastDiv fast_div(uint32_t d) {  // d >= 2
 
 constexpr int kNormMaxVec = 512 * 8 * 10;  // longest row that rms_norm_kernel holds in registers
 
+// Behind norm_order_kernel the norm is its programmatic dependent.
+template <typename K>
+safe_status norm_launch(K kernel, int64_t ctas, int threads, const NormParams& p, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.mark != nullptr ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return SAFE_ERR_CUDA;
+  return launch_status();
+}
+
 template <typename T, int kMode, int NV, int TPR>
 safe_status norm_launch(const NormParams& p, cudaStream_t s) {
   constexpr int rows_cta = TPR <= 32 ? 128 / TPR : 1;
-  rms_norm_kernel<T, kMode, NV, TPR>
-      <<<static_cast<unsigned>((p.rows_pad + rows_cta - 1) / rows_cta), TPR <= 32 ? 128 : TPR, 0, s>>>(p);
-  return launch_status();
+  return norm_launch(rms_norm_kernel<T, kMode, NV, TPR>, (p.rows_pad + rows_cta - 1) / rows_cta, TPR <= 32 ? 128 : TPR, p, s);
 }
 
 // The fewest threads that hold a row in a few units each: part of a warp for
@@ -553,8 +567,7 @@ safe_status launch_norm(const NormParams& p, int mode, cudaStream_t s) {
   if (p.D <= 32 * 10) return norm_launch<T, kNormOne, 10, 32>(p, s);
   if (p.D <= 128 * 10) return norm_launch<T, kNormOne, 10, 128>(p, s);
   if (p.D <= 128 * 20) return norm_launch<T, kNormOne, 20, 128>(p, s);
-  rms_norm_long_kernel<T><<<static_cast<unsigned>(p.rows), 512, 0, s>>>(p);
-  return launch_status();
+  return norm_launch(rms_norm_long_kernel<T>, p.rows, 512, p, s);
 }
 
 template <typename T>
@@ -1202,6 +1215,15 @@ safe_status safe_rms_norm(const void* x, int x_full, const void* res, const int3
   p.rows_pad = q != nullptr ? (p.rows + 127) / 128 * 128 : p.rows;
   p.inv_D = 1.f / static_cast<float>(D);
   p.by_R = fast_div(static_cast<uint32_t>(R > 1 ? R : 2));
+  if (h_full && R > 1) {
+    uint8_t* mark = static_cast<uint8_t*>(y != nullptr ? y : q);
+    p.mark = mark;
+    p.mark_pitch = static_cast<size_t>(D) * (y != nullptr ? e : 1);
+    const dim3 grid(static_cast<unsigned>((R + 1023LL) / 1024), static_cast<unsigned>(B));
+    norm_order_kernel<<<grid, 1024, 0, as_stream(stream)>>>(S, R, mark, p.mark_pitch);
+    const safe_status st = launch_status();
+    if (st != SAFE_OK) return st;
+  }
   switch (dtype) {
     case SAFE_F32: return launch_norm<float>(p, mode, as_stream(stream));
     case SAFE_F16: return launch_norm<__half>(p, mode, as_stream(stream));
