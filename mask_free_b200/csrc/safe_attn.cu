@@ -1185,10 +1185,13 @@ safe_status safe_rms_norm(const void* x, int x_full, const void* res, const int3
   if (clash(y, ob, x, xb) || clash(y, ob, res, rb) || clash(h, h_full ? 0 : ob, x, xb) ||
       clash(h, h_full ? 0 : ob, res, rb) || overlap(h, h_full ? rb : ob, y, ob) || (h_full && overlap(h, rb, x, xb)))
     return SAFE_ERR_INVALID_ARG;
+  const size_t hb = h_full ? rb : ob, wb = static_cast<size_t>(D) * 4, Sb = static_cast<size_t>(p.rows) * 4;
+  if (overlap(y, ob, w, wb) || overlap(h, hb, w, wb) || overlap(y, ob, S, Sb) || overlap(h, hb, S, Sb))
+    return SAFE_ERR_INVALID_ARG;
   if (q != nullptr) {
-    const void* in[] = {x, res, w, h, y};
-    const size_t len[] = {xb, rb, static_cast<size_t>(D) * 4, h_full ? rb : ob, ob};
-    for (int i = 0; i < 5; ++i)
+    const void* in[] = {x, res, S, w, h, y};
+    const size_t len[] = {xb, rb, Sb, wb, hb, ob};
+    for (int i = 0; i < 6; ++i)
       if (overlap(q, n_rows, in[i], len[i]) || overlap(q_scales, sb, in[i], len[i])) return SAFE_ERR_INVALID_ARG;
     if (overlap(q, n_rows, q_scales, sb)) return SAFE_ERR_INVALID_ARG;
   }
