@@ -470,7 +470,7 @@ safe_status safe_mx_dequantize(const void* data, const void* scales, int fmt, fl
  *  Wt, Wt_scales  device: d_out x d_in.
  *  bias  device fp32 [d_out] (4-byte aligned) or NULL; act as
  *        safe_gather_linear (0 = none, 1 = tanh-GELU).
- *  Y     device bf16 [rows, d_out] (written; apart from the operands).
+ *  Y     device bf16 [rows, d_out] (written; apart from the operands and bias).
  *  ws    device workspace of safe_mx_linear_workspace_bytes bytes (32-byte
  *        aligned; caller-owned, contents undefined after the call) or NULL:
  *        with it, the tiles of the last, partial wave of CTAs are computed in

@@ -1389,7 +1389,8 @@ safe_status safe_mx_linear(const void* X, const void* X_scales, const void* Wt, 
   if (overlap(Y, yb, X, static_cast<size_t>(rows) * row_bytes) ||
       overlap(Y, yb, X_scales, safe_mx_scale_bytes(rows, d_in, fmt)) ||
       overlap(Y, yb, Wt, static_cast<size_t>(d_out) * row_bytes) ||
-      overlap(Y, yb, Wt_scales, safe_mx_scale_bytes(d_out, d_in, fmt)))
+      overlap(Y, yb, Wt_scales, safe_mx_scale_bytes(d_out, d_in, fmt)) ||
+      overlap(Y, yb, bias, static_cast<size_t>(d_out) * 4))
     return SAFE_ERR_INVALID_ARG;
   const int pairs = mx_linear_pairs(fmt);
   MxPlan plan = mx_linear_plan(rows, d_out, row_bytes, pairs, ws != nullptr);

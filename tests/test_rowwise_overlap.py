@@ -37,3 +37,12 @@ def test_norm_outputs_over_w_or_S(lib):
     quant = dict(q=at(6), qs=at(7))
     assert call(**rows, q=at(5), qs=at(7), y=None) == INVALID and call(**rows, q=at(6), qs=at(5), y=None) == INVALID
     assert call(**quant, y=None, w=off(6, 16)) == INVALID
+
+
+def test_layer_output_over_bias(lib):
+    def call(Y=at(4), bias=at(5), rows=16, o=64, fmt=0):
+        return lib.safe_mx_linear(at(0), at(1), at(2), at(3), fmt, 1.0, bias, 0, Y, rows, 64, o, None, 0, None)
+
+    for fmt in (0, 1, 2):
+        assert call(bias=at(4), fmt=fmt) == INVALID and call(Y=off(5, 240), fmt=fmt) == INVALID
+        assert call(bias=off(4, 16 * 64 * 2 - 4), fmt=fmt) == INVALID
