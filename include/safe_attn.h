@@ -446,8 +446,8 @@ safe_status safe_rope(const void* q, const int64_t q_strides[3], void* oq, const
  *  X      device [B, N, D], dtype SAFE_F32 / SAFE_F16 / SAFE_BF16.
  *  S      device int32 [B, k], any order (an index outside [0, N) is flagged
  *         and replaced by row 0), or NULL: every row (k ignored).
- *  data, scales  device, of B * (k or N) rows (written); apart from X and
- *         from each other. X, data and scales are 16-byte aligned.
+ *  data, scales  device, of B * (k or N) rows (written); apart from X, S and
+ *         each other. X, data and scales are 16-byte aligned.
  * safe_mx_dequantize: the values of `rows` rows, rounded to Y's dtype (Y
  * device [rows, D], 16-byte aligned).
  * safe_mx_scale_bytes returns 0 for sizes that have no such form.

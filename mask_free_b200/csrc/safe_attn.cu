@@ -1334,6 +1334,8 @@ safe_status safe_mx_quantize(const void* X, int dtype, const int32_t* S, int k, 
   const size_t db = static_cast<size_t>(p.rows) * (fmt == SAFE_MXFP8 ? D : D / 2);
   const size_t sb = safe_mx_scale_bytes(p.rows, D, fmt), xb = static_cast<size_t>(B) * N * D * float_size(dtype);
   if (overlap(data, db, X, xb) || overlap(scales, sb, X, xb) || overlap(data, db, scales, sb)) return SAFE_ERR_INVALID_ARG;
+  const size_t Sb = static_cast<size_t>(p.rows) * 4;
+  if (overlap(data, db, S, Sb) || overlap(scales, sb, S, Sb)) return SAFE_ERR_INVALID_ARG;
   switch (dtype) {
     case SAFE_F32: return launch_mx_quantize<float>(p, fmt, as_stream(stream));
     case SAFE_F16: return launch_mx_quantize<__half>(p, fmt, as_stream(stream));

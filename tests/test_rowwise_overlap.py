@@ -46,3 +46,13 @@ def test_layer_output_over_bias(lib):
     for fmt in (0, 1, 2):
         assert call(bias=at(4), fmt=fmt) == INVALID and call(Y=off(5, 240), fmt=fmt) == INVALID
         assert call(bias=off(4, 16 * 64 * 2 - 4), fmt=fmt) == INVALID
+
+
+def test_quantised_rows_over_S(lib):
+    def call(S=at(3), k=4, data=at(1), sc=at(2), fmt=0, B=2):
+        return lib.safe_mx_quantize(at(0), 4, S, k, fmt, 1.0, data, sc, B, 16, 64, None)
+
+    for fmt in (0, 1, 2):
+        assert call(data=at(3), fmt=fmt) == INVALID and call(sc=at(3), fmt=fmt) == INVALID
+        assert call(data=off(3, 16), fmt=fmt) == INVALID and call(S=off(2, 508), fmt=fmt) == INVALID
+        assert call(S=off(1, 2 * 4 * (64 if fmt == 0 else 32) - 4), fmt=fmt) == INVALID
