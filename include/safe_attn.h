@@ -399,7 +399,8 @@ safe_status safe_rms_norm(const void* x, int x_full, const void* res, const int3
  *         itself (same strides: in place) or shares no element with the
  *         inputs, and none with the other output or within itself: tensors
  *         apart, or views side by side in the rows of one fused tensor (other
- *         interleavings are refused).
+ *         interleavings are refused). freq, pos and S lie outside the range
+ *         from an output's first element to its last.
  *  dtype  SAFE_F32 / SAFE_F16 / SAFE_BF16.
  *  freq   device int64 [r / 2]: f_i / (2 pi) in units of 2^-64 turns (modulo
  *         one turn). pos * freq modulo 2^64 is the exact phase, at any

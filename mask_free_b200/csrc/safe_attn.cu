@@ -1287,6 +1287,14 @@ safe_status safe_rope(const void* q, const int64_t q_strides[3], void* oq, const
     for (int j = 0; j < n; ++j)
       if ((i != j || !in_place[i]) && !apart(out[i], in[j], e)) return SAFE_ERR_INVALID_ARG;
   if (n == 2 && !apart(out[0], out[1], e)) return SAFE_ERR_INVALID_ARG;
+  // nor with freq, pos or S
+  for (int i = 0; i < n; ++i) {
+    const size_t ob = static_cast<size_t>(extent(out[i], true, true)) * e;
+    if (overlap(os[i], ob, freq, static_cast<size_t>(r / 2) * 8) ||
+        overlap(os[i], ob, pos, static_cast<size_t>(pos_batched ? B : 1) * N * axes * 4) ||
+        overlap(os[i], ob, S, static_cast<size_t>(B) * R * 4))
+      return SAFE_ERR_INVALID_ARG;
+  }
   p.freq = reinterpret_cast<const long long*>(freq);
   p.pos = pos;
   p.pos_b = pos_batched ? static_cast<long long>(N) * axes : 0;

@@ -56,3 +56,22 @@ def test_quantised_rows_over_S(lib):
         assert call(data=at(3), fmt=fmt) == INVALID and call(sc=at(3), fmt=fmt) == INVALID
         assert call(data=off(3, 16), fmt=fmt) == INVALID and call(S=off(2, 508), fmt=fmt) == INVALID
         assert call(S=off(1, 2 * 4 * (64 if fmt == 0 else 32) - 4), fmt=fmt) == INVALID
+
+
+def test_rope_outputs_over_freq_pos_or_S(lib):
+    i3, fused = ctypes.c_int64 * 3, (16 * 640, 640, 64)
+
+    def call(q=at(0), qs=None, oq=at(1), oqs=None, ok=at(3), freq=at(4), pos=None, batched=0, S=None, sec=(32,), R=16):
+        i3n = lambda v: None if v is None else i3(*v)
+        return lib.safe_rope(q, i3n(qs), oq, i3n(oqs), 4, at(2), None, ok, None, 2, 4, ctypes.cast(freq, ops._i64p),
+                             (ctypes.c_int32 * len(sec))(*sec), len(sec), pos, batched, S, 2, 16, R, 64, 64, 0, 1.0, None)
+
+    qb, kb = 2 * 16 * 4 * 64 * 2, 2 * 16 * 2 * 64 * 2
+    assert call(freq=at(1)) == INVALID and call(freq=off(1, qb - 8)) == INVALID and call(freq=off(3, kb - 8)) == INVALID
+    assert call(oq=off(4, 240)) == INVALID  # freq: 256 bytes
+    assert call(pos=at(3)) == INVALID and call(pos=off(1, qb - 4)) == INVALID and call(ok=off(6, 48), pos=at(6)) == INVALID
+    two = dict(sec=(16, 16), pos=at(6))     # 128 bytes shared, 256 batched
+    assert call(ok=off(6, 112), **two) == INVALID and call(ok=off(6, 240), batched=1, **two) == INVALID
+    rows = dict(pos=at(6), S=at(5))         # 128 bytes
+    assert call(ok=at(5), **rows) == INVALID and call(oq=off(5, 112), **rows) == INVALID
+    assert call(q=at(0), qs=fused, oq=at(0), oqs=fused, freq=off(0, 2 * 16 * 640 * 2 - 6 * 64 * 2 - 8)) == INVALID
