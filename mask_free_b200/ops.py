@@ -609,7 +609,8 @@ class MxTensor:
     data's leading dims one after another; layout: safe_mx_quantize in
     include/safe_attn.h), `fmt` "mxfp8", "mxfp4" or "nvfp4", and `scale` the
     factor of the whole matrix (nvfp4; 1 otherwise). Checked once, here: its
-    parts cannot be exchanged afterwards."""
+    parts cannot be exchanged afterwards; a call that takes it as `out` fills
+    it anew, with its factor."""
 
     __slots__ = ("_data", "_scales", "_fmt", "_scale", "_rows", "_D")
 
@@ -656,7 +657,8 @@ def mx_scale_bytes(rows: int, D: int, fmt: str) -> int:
 
 def _mx_out(out, lead, D: int, fmt: str, scale: float, like) -> MxTensor:
     """A microscaled matrix [*lead, D] on the device of `like`: one of undefined
-    contents, or the given one checked."""
+    contents, or the given one checked (its factor is set behind the call that
+    fills it: a refused one leaves it as it was)."""
     if out is None:
         m = MxTensor.__new__(MxTensor)  # made to fit: nothing to check
         rows = math.prod(lead)
@@ -669,7 +671,6 @@ def _mx_out(out, lead, D: int, fmt: str, scale: float, like) -> MxTensor:
         return m
     if not isinstance(out, MxTensor) or out.fmt != fmt or out.shape != (*lead, D) or out.device != like.device:
         raise ValueError(f"out must be an MxTensor {fmt} of shape {(*lead, D)} on {like.device}")
-    out._scale = scale
     return out
 
 
@@ -937,6 +938,7 @@ def mx_quantize(x, fmt: str, S=None, scale: float = 1.0, out=None) -> MxTensor:
     m = _mx_out(out, (B, R) if nd == 3 else (N,), D, fmt, g, x)
     _run("safe_mx_quantize", dev, x.data_ptr(), dt, _ptr(S), k, code, g, m._data.data_ptr(), m._scales.data_ptr(), B, N,
          D)
+    m._scale = g
     return m
 
 

@@ -1,12 +1,15 @@
 """Host-side refusals of the row-wise entry points (no GPU): outputs over the
-arrays that a call reads, and sizes past the counters."""
+arrays that a call reads, sizes past the counters, and what a refused call
+leaves behind."""
 
 import ctypes
 
 import pytest
+import torch
 
 from mask_free_b200 import build as B_
 from mask_free_b200 import ops
+from tests.test_binding_checks import rec, t  # noqa: F401
 from tests.test_rowwise_checks import at
 
 INVALID, UNSUPPORTED = 1, 2
@@ -75,3 +78,18 @@ def test_rope_outputs_over_freq_pos_or_S(lib):
     rows = dict(pos=at(6), S=at(5))         # 128 bytes
     assert call(ok=at(5), **rows) == INVALID and call(oq=off(5, 112), **rows) == INVALID
     assert call(q=at(0), qs=fused, oq=at(0), oqs=fused, freq=off(0, 2 * 16 * 640 * 2 - 6 * 64 * 2 - 8)) == INVALID
+
+
+def test_a_refused_call_leaves_out_as_it_was(rec, monkeypatch):
+    x, out = t(2, 8, 64), ops.MxTensor(torch.zeros((2, 8, 32), dtype=torch.uint8),
+                                       torch.zeros(ops.mx_scale_bytes(16, 64, "nvfp4"), dtype=torch.uint8), "nvfp4", 0.5)
+
+    def refuse(name, *args):
+        raise ops.SafeError(name, INVALID)
+
+    with monkeypatch.context() as m:
+        m.setattr(ops, "_run", refuse)
+        with pytest.raises(ops.SafeError):
+            ops.mx_quantize(x, "nvfp4", scale=0.25, out=out)
+    assert out.scale == 0.5  # the old elements keep their factor
+    assert ops.mx_quantize(x, "nvfp4", scale=0.25, out=out) is out and out.scale == 0.25
