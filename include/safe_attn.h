@@ -478,8 +478,8 @@ safe_status safe_mx_dequantize(const void* data, const void* scales, int fmt, fl
  *        pieces along d_in and added by a second kernel (fp32, in a fixed
  *        order). The size is 0 where that does not pay off; without it, or
  *        with less, every tile is computed whole.
- *  d_in >= 64 a multiple of 32, d_out >= 8 a multiple of 8; all pointers but
- *  bias 16-byte aligned.
+ *  d_in a multiple of 32 from 64 to 2^20, d_out >= 8 a multiple of 8; all
+ *  pointers but bias 16-byte aligned.
  */
 size_t safe_mx_linear_workspace_bytes(int64_t rows, int d_in, int d_out, int fmt);
 safe_status safe_mx_linear(const void* X, const void* X_scales, const void* Wt, const void* Wt_scales, int fmt,

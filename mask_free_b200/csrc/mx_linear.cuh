@@ -163,7 +163,7 @@ struct MxLinearParams {
   // nvfp4, 12800 x 9216 x 6912.)
   int whole, units;
   float* part;
-  uint16_t piece_tile[kMxPieces], piece_k0[kMxPieces], piece_n[kMxPieces];  // tile, first stage, stages
+  uint16_t piece_tile[kMxPieces], piece_k0[kMxPieces], piece_n[kMxPieces];  // tile, first stage, stages (8192 at most)
 };
 
 constexpr int kMxThreads = 640;  // warps 0-3 producers / MMA / TMEM, warps 4-19 epilogue

@@ -711,8 +711,7 @@ MxPlan mx_linear_plan(int64_t M, int d_out, int row_bytes, int pairs, bool may_s
   if (split > nk / 4) split = nk / 4;  // pieces of four stages at least
   const int64_t row_tiles = (M + 255) / 256, rows = M / row_tiles;  // of a tile, on average
   const int64_t cost = 12 + 28 * rows * rest * split / (64 * 256);
-  if (!may_split || split < 2 || nk - (nk + split - 1) / split <= cost || tiles > INT_MAX || rest * split > kMxPieces ||
-      nk > 65535)
+  if (!may_split || split < 2 || nk - (nk + split - 1) / split <= cost || tiles > INT_MAX || rest * split > kMxPieces)
     split = 1;
   p.split = split;
   p.rest = split > 1 ? rest : 0;
@@ -1379,8 +1378,8 @@ safe_status safe_mx_dequantize(const void* data, const void* scales, int fmt, fl
 }
 
 size_t safe_mx_linear_workspace_bytes(int64_t rows, int d_in, int d_out, int fmt) {
-  if (fmt < SAFE_MXFP8 || fmt > SAFE_NVFP4 || rows < 1 || rows > kMxMaxRows || d_in < 64 || d_in % 32 != 0 || d_out < 8 ||
-      d_out > kMxMaxRows || d_out % 8 != 0)
+  if (fmt < SAFE_MXFP8 || fmt > SAFE_NVFP4 || rows < 1 || rows > kMxMaxRows || d_in < 64 || d_in > kMxMaxD ||
+      d_in % 32 != 0 || d_out < 8 || d_out > kMxMaxRows || d_out % 8 != 0)
     return 0;
   return mx_linear_plan(rows, d_out, fmt == SAFE_MXFP8 ? d_in : d_in / 2, mx_linear_pairs(fmt), true).part_bytes;
 }
@@ -1393,7 +1392,8 @@ safe_status safe_mx_linear(const void* X, const void* X_scales, const void* Wt, 
     return SAFE_ERR_INVALID_ARG;
   if (fmt < SAFE_MXFP8 || fmt > SAFE_NVFP4 || !std::isnormal(alpha) || (act != 0 && act != 1)) return SAFE_ERR_INVALID_ARG;
   if (rows < 1 || rows > INT_MAX || d_in < 64 || d_in % 32 != 0 || d_out < 8 || d_out % 8 != 0) return SAFE_ERR_INVALID_ARG;
-  if (rows > kMxMaxRows || d_out > kMxMaxRows) return SAFE_ERR_UNSUPPORTED;
+  // a tile's stages, which the epilogue waits for at once, take 3 ms at the largest d_in
+  if (rows > kMxMaxRows || d_out > kMxMaxRows || d_in > kMxMaxD) return SAFE_ERR_UNSUPPORTED;
   const int row_bytes = fmt == SAFE_MXFP8 ? d_in : d_in / 2;
   const size_t yb = static_cast<size_t>(rows) * d_out * 2;
   if (overlap(Y, yb, X, static_cast<size_t>(rows) * row_bytes) ||

@@ -93,3 +93,15 @@ def test_a_refused_call_leaves_out_as_it_was(rec, monkeypatch):
             ops.mx_quantize(x, "nvfp4", scale=0.25, out=out)
     assert out.scale == 0.5  # the old elements keep their factor
     assert ops.mx_quantize(x, "nvfp4", scale=0.25, out=out) is out and out.scale == 0.25
+
+
+def test_layers_of_rows_past_the_counters(lib):
+    far = [ctypes.c_void_p((i + 1) << 44) for i in range(6)]
+
+    def call(fmt, d_in, ws=None, wb=0):
+        return lib.safe_mx_linear(far[0], far[1], far[2], far[3], fmt, 1.0, None, 0, far[4], 16, d_in, 64, ws, wb, None)
+
+    for fmt in (0, 1, 2):
+        for d_in in (2 ** 31 - 32, 2 ** 31 - 128, 2 ** 30, 2 ** 20 + 32):  # the rows that quantising takes end at 2^20
+            assert call(fmt, d_in) == UNSUPPORTED and call(fmt, d_in, far[5], 1 << 40) == UNSUPPORTED
+            assert lib.safe_mx_linear_workspace_bytes(16, d_in, 64, fmt) == 0
