@@ -585,6 +585,12 @@ def _new(shape, dtype, dev) -> torch.Tensor:
     return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _check_ints(*sizes):
+    """Sizes that go to the library as ints (ctypes would drop their upper bits)."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"sizes above 2^31 - 1 are not supported, got {sizes}")
+
+
 def _float_code(t, name: str) -> int:
     if not isinstance(t, torch.Tensor) or t.dtype not in _FLOATS:
         raise ValueError(f"{name} must be a float32, float16 or bfloat16 tensor")
@@ -693,6 +699,7 @@ def rms_norm(x, w=None, residual=None, S=None, eps=1e-6, x_compact=False, quant=
     if residual is not None and (not isinstance(residual, torch.Tensor) or residual.dim() != 3):
         _need(residual, "residual", dtype, 3, device=dev)
     B, N, D = x.shape if residual is None else residual.shape
+    _check_ints(B, N, D)
     k, full = 0, False
     if S is None:
         R = N
@@ -873,6 +880,7 @@ def rope(q, k, table: RopeTable, pos=None, S=None, interleaved=False, inplace=Fa
         sp = S.data_ptr()
     elif N != R:
         raise ValueError(f"pos has {N} tokens, q {R} rows")
+    _check_ints(B, N, H, Hk, d)
     if inplace:
         if out is not None:
             raise ValueError("inplace writes to q and k: out must be None")
@@ -929,6 +937,7 @@ def mx_quantize(x, fmt: str, S=None, scale: float = 1.0, out=None) -> MxTensor:
     B, N, D = x.shape if nd == 3 else (1, *x.shape)
     if D < 32 or D % 32:
         raise ValueError(f"rows must have a multiple of 32 elements, got {D}")
+    _check_ints(B, N, D)
     dev, g, k = x.device, _factor(fmt, scale), 0
     R = N
     if S is not None:
@@ -949,6 +958,7 @@ def mx_dequantize(m: MxTensor, dtype=torch.bfloat16, out=None):
     if dtype not in _FLOATS:
         raise ValueError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
     data, D = m._data, m._D
+    _check_ints(D)
     out = _out_like(out, "out", m._scales, dtype, (*data.shape[:-1], D))
     _run("safe_mx_dequantize", data.device, data.data_ptr(), m._scales.data_ptr(), _FORMATS[m._fmt], m._scale,
          out.data_ptr(), _FLOATS[dtype], m._rows, D)
@@ -958,6 +968,7 @@ def mx_dequantize(m: MxTensor, dtype=torch.bfloat16, out=None):
 def mx_linear_workspace_bytes(rows: int, d_in: int, d_out: int, fmt: str) -> int:
     if fmt not in _FORMATS:
         raise ValueError(f"fmt must be one of {sorted(_FORMATS)}, got {fmt!r}")
+    _check_ints(d_in, d_out)
     return int(lib().safe_mx_linear_workspace_bytes(rows, d_in, d_out, _FORMATS[fmt]))
 
 
@@ -976,6 +987,7 @@ def mx_linear(X: MxTensor, W: MxTensor, bias=None, act="none", out=None, ws=None
     rows, d_in, d_out, dev = X._rows, X._D, W._rows, x.device
     if w.dim() != 2 or W._D != d_in or w.device != dev:
         raise ValueError(f"W must be [d_out, {d_in}] on {dev}, got {W.shape} on {W.device}")
+    _check_ints(d_in, d_out)
     if bias is not None:
         _check_tensor(bias, "bias", torch.float32, (d_out,), dev)
     if act not in _ACTS:

@@ -105,3 +105,44 @@ def test_layers_of_rows_past_the_counters(lib):
         for d_in in (2 ** 31 - 32, 2 ** 31 - 128, 2 ** 30, 2 ** 20 + 32):  # the rows that quantising takes end at 2^20
             assert call(fmt, d_in) == UNSUPPORTED and call(fmt, d_in, far[5], 1 << 40) == UNSUPPORTED
             assert lib.safe_mx_linear_workspace_bytes(16, d_in, 64, fmt) == 0
+
+
+def test_sizes_that_an_int_cannot_hold_are_refused(rec):
+    # the entry points' sizes are ints: 2^32 + 5 rows must not run as 5
+    big = 2 ** 32 + 5
+
+    def m(*shape, dtype=torch.bfloat16):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    i32, u8 = torch.int32, torch.uint8
+    for shape in ((1, big, 1), (big, 1, 1), (1, 1, big)):
+        with pytest.raises(ValueError):
+            ops.rms_norm(m(*shape))
+    with pytest.raises(ValueError):
+        ops.rms_norm(m(1, 3, 1), residual=m(1, big, 1), S=m(1, 3, dtype=i32), x_compact=True)
+    tab = ops.RopeTable(torch.zeros(1, dtype=torch.int64, device="meta"), [1])
+    for q, k in ((m(1, big, 1, 2), None), (m(big, 1, 1, 2), None), (m(1, 1, big, 2), None), (m(1, 1, 1, 2), m(1, 1, big, 2)),
+                 (m(1, 1, 1, big + 1), None)):
+        with pytest.raises(ValueError):
+            ops.rope(q, k, tab)
+    with pytest.raises(ValueError):
+        ops.rope(m(1, 3, 1, 2), None, tab, pos=m(big, 1, dtype=i32), S=m(1, 3, dtype=i32))
+    wide = 2 ** 32 + 64
+    for fmt in ("mxfp8", "mxfp4", "nvfp4"):
+        for shape in ((1, big, 64), (big, 1, 64), (1, 1, wide), (big, 64)):
+            with pytest.raises(ValueError):
+                ops.mx_quantize(m(*shape), fmt)
+
+        def mx(rows, D):
+            data = m(rows, D, dtype=torch.float8_e4m3fn) if fmt == "mxfp8" else m(rows, D // 2, dtype=u8)
+            return ops.MxTensor(data, m(ops.mx_scale_bytes(rows, D, fmt), dtype=u8), fmt)
+
+        with pytest.raises(ValueError):
+            ops.mx_dequantize(mx(1, wide))
+        for X, W in ((mx(1, wide), mx(8, wide)), (mx(1, 64), mx(2 ** 32 + 8, 64))):
+            with pytest.raises(ValueError):
+                ops.mx_linear(X, W, ws=False)
+        for sizes in ((1, wide, 8), (1, 64, 2 ** 32 + 8)):
+            with pytest.raises(ValueError):
+                ops.mx_linear_workspace_bytes(*sizes, fmt)
+    assert rec.calls == []
