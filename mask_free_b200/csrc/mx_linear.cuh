@@ -17,12 +17,15 @@
 // MMAs of one thread run in order, so one scale buffer serves every stage.
 // TMEM (512 columns): the last 64 hold the scales; the two accumulators of
 // 256 columns (tile i uses i & 1) overlap in 64 columns in the middle, the last
-// of accumulator 0 and the first of 1. In the last stage of a tile the MMAs
-// of these shared columns come first, in the first stage of the next they
-// come last, so that the epilogue reads them while the other 192 columns are
-// multiplied, and the tensor core does not wait for it. (For these two stages
-// each CTA holds 96 + 32 rows of W, its halves of the two parts, instead of
-// 128: the columns' order stays that of the rows of W.)
+// of accumulator 0 and the first of 1. A tile's first MMA waits until the
+// epilogue has read these from the tile before, which it does first of all;
+// the other 192 columns are read while the next tile is multiplied.
+// Every MMA of a tile has the same shape and accumulator: consecutive ones of one
+// thread are ordered under that condition only (a form whose first and last
+// stages did the shared columns apart, to hide that wait, added to them in two
+// shapes; with a wait for completion wherever the shape changes it was slower
+// than this one, as was that with both shapes in every stage: nvfp4
+// 51200 x 2304 x 6912 336 and 328 us against 301).
 //
 // What bounds it: a stage is 34 - 38 KB into shared memory and as much out of
 // it for 512 cycles of MMA, and 1000 W. A call by itself (PFLOP/s; 51200 rows at
@@ -145,7 +148,6 @@ constexpr int kMxPieces = 96;  // pieces at most
 struct MxLinearParams {
   CUtensorMap x_map;   // bytes [M, row bytes], box 128 x 128, 128B swizzle
   CUtensorMap w_map;   // bytes [d_out, row bytes], box 128 x 128, 128B swizzle
-  CUtensorMap w96_map, w32_map;  // the same, boxes 128 x 96 and 128 x 32
   CUtensorMap xs_map;  // scale tiles as 8-byte words [row blocks, tiles * 64], box (tiles of a stage * 64) x 1
   CUtensorMap ws_map;  // the same of W, box (tiles of a stage * 64) x 2
   const float* bias;   // [d_out] or null
@@ -250,8 +252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   uint64_t* empty = full + ST;                                     // [ST] stage consumed
   uint64_t* acc_full = empty + ST;                                 // [2] accumulator complete
   uint64_t* acc_empty = acc_full + 2;                              // [2] accumulator read back (rank 0)
-  uint64_t* sh_full = acc_empty + 2;                               // the shared columns complete
-  uint64_t* sh_empty = sh_full + 1;                                // the shared columns read back (rank 0)
+  uint64_t* sh_empty = acc_empty + 2;                              // the shared columns read back (rank 0)
   uint64_t* drain = sh_empty + 1;                                  // MMA abort path
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   __shared__ int abort_flag;
@@ -273,7 +274,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       mbar_init(&acc_full[a], 1);
       mbar_init(&acc_empty[a], 24);  // the epilogue warps of both CTAs that read its own columns
     }
-    mbar_init(sh_full, 1);
     mbar_init(sh_empty, 8);  // the epilogue warps that read them
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -309,10 +309,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     if (leader) {
       tma_prefetch_desc(elements ? &p.x_map : &p.xs_map);
       tma_prefetch_desc(elements ? &p.w_map : &p.ws_map);
-      if (elements) {
-        tma_prefetch_desc(&p.w96_map);
-        tma_prefetch_desc(&p.w32_map);
-      }
     }
     const uint32_t full0 = cluster_addr(full, 0);  // the even CTA's stage barriers
     const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB), sa0 = smem_u32(sSA), sb0 = smem_u32(sSB);
@@ -326,8 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       const int k0 = piece < 0 ? 0 : p.piece_k0[piece], n = piece < 0 ? nk : p.piece_n[piece];
       // this CTA's rows and columns; rows past the matrix are zero fill and not stored
       const int r0 = (t / p.n_tiles) * 256 + 128 * static_cast<int>(rank);
-      const int n0 = nt * kMxTileN, rk = static_cast<int>(rank);
-      const int own = n0 + (i & 1 ? 64 : 0) + 96 * rk, shared = n0 + (i & 1 ? 0 : 192) + 32 * rk;
+      const int n0 = nt * kMxTileN, w0 = n0 + 128 * static_cast<int>(rank);
       for (int kc = 0; kc < n; ++kc) {
         if (issued >= ST && !warp_wait_short(&empty[s], wrap, &abort_flag)) {
           ok = false;
@@ -337,12 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         if (elements) {
           if (expect) mbar_arrive_expect_tx(&full[s], 2 * mx_stage_bytes(kFmt));
           tma_load_2d_pair_if(leader, a0 + s * kMxABytes, &p.x_map, bar, 128 * (k0 + kc), r0);
-          if (kc == 0 || kc == n - 1) {
-            tma_load_2d_pair_if(leader, b0 + s * kMxBBytes, &p.w96_map, bar, 128 * (k0 + kc), own);
-            tma_load_2d_pair_if(leader, b0 + s * kMxBBytes + 96 * 128, &p.w32_map, bar, 128 * (k0 + kc), shared);
-          } else {
-            tma_load_2d_pair_if(leader, b0 + s * kMxBBytes, &p.w_map, bar, 128 * (k0 + kc), n0 + 128 * rk);
-          }
+          tma_load_2d_pair_if(leader, b0 + s * kMxBBytes, &p.w_map, bar, 128 * (k0 + kc), w0);
         } else {
           tma_load_2d_pair_if(leader, sa0 + s * kSfA, &p.xs_map, bar, 64 * KT * (k0 + kc), r0 >> 7);
           tma_load_2d_pair_if(leader, sb0 + s * kSfB, &p.ws_map, bar, 64 * KT * (k0 + kc), n0 >> 7);
@@ -382,7 +372,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       }
       tc_fence_after();
       const uint32_t tacc = tbase + 192 * a;
-      const uint32_t down = 64 * a, dshared = 192 * (a ^ 1);  // first columns of the own and of the shared part
       const int piece = pair + i * n_pairs - p.whole;
       const int n = piece < 0 ? nk : p.piece_n[piece];
       const int last = piece < 0 || p.piece_k0[piece] + n == nk ? last_steps : 4;
@@ -402,43 +391,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           tmem_copy_scales_pair_if(leader, sfb + 8 * j, at(dSB, lsb + 32 * j));
           tmem_copy_scales_pair_if(leader, sfb + 8 * j + 4, at(dSB, lsb + 32 * (KT + j)));
         }
-        const int steps = kc == n - 1 ? last : 4;
-        const uint32_t acc = kc != 0 ? 1u : 0u;
-        auto mma = [&](int kk, uint32_t d, uint32_t b, uint32_t sf, int N) {
-          // scale tile and byte of step kk
-          constexpr int per = 4 / KT;  // steps that share a tile
-          const int j = kk / per, id = kFmt == kMxFp8 ? kk : kFmt == kMxFp4 ? 2 * (kk & 1) : 0;
-          umma_pair_mx_if<kFmt>(kk < steps ? leader : 0u, d, at(dA, la + 2 * kk), at(dB, b + 2 * kk),
-                                make_idesc_mx(kFmt, 256, N, id), sfa + 4 * j, sf + 8 * j, kk != 0 ? 1u : acc);
-        };
-        auto all = [&] {
+        auto mma = [&](int steps, uint32_t acc) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma(kk, tacc, lb, sfb, 256);
-        };
-        auto own = [&] {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma(kk, tacc + down, lb, sfb + (down >> 5), 192);
-        };
-        auto shared = [&] {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma(kk, tacc + dshared, lb + (96 * 128 >> 4), sfb + (dshared >> 5), 64);
+          for (int kk = 0; kk < 4; ++kk) {
+            // scale tile and byte of step kk
+            constexpr int per = 4 / KT;  // steps that share a tile
+            const int j = kk / per, id = kFmt == kMxFp8 ? kk : kFmt == kMxFp4 ? 2 * (kk & 1) : 0;
+            umma_pair_mx_if<kFmt>(kk < steps ? leader : 0u, tacc, at(dA, la + 2 * kk), at(dB, lb + 2 * kk),
+                                  make_idesc_mx(kFmt, 256, 256, id), sfa + 4 * j, sfb + 8 * j, kk != 0 ? 1u : acc);
+          }
         };
         auto shared_read = [&] {  // the last tile's shared columns have been read
           ok = i == 0 || warp_wait_short(sh_empty, (i - 1) & 1, &abort_flag);
           tc_fence_after();
           return ok;
         };
+        // The stages between the first and the last of a tile get constants: with
+        // one path for all, each MMA's two predicates cost more than they look
+        // (nvfp4 51200 x 2304 x 6912 339 us instead of 308, mxfp8 595 instead of 544).
         if (kc == n - 1) {
           if (kc == 0 && !shared_read()) break;
-          shared();
-          umma_pair_commit_both_if(leader, smem_u32(sh_full));
-          own();
+          mma(last, kc != 0 ? 1u : 0u);
         } else if (kc == 0) {
-          own();
           if (!shared_read()) break;
-          shared();
+          mma(4, 0u);
         } else {
-          all();
+          mma(4, 1u);
         }
         // both CTAs' stage may be refilled once these copies and MMAs have read it
         umma_pair_commit_both_if(leader, smem_u32(&empty[s]));
@@ -483,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       bias2[lane] = next;
       next = load_bias(i + 1);
       const bool sh = e == (a ? 0 : 3);
-      if (!warp_wait_short(sh ? sh_full : &acc_full[a], sh ? i & 1 : (i >> 1) & 1, &abort_flag)) break;
+      if (!warp_wait_short(&acc_full[a], (i >> 1) & 1, &abort_flag)) break;
       tc_fence_after();
       uint32_t v[64];
       tmem_ld32(lane_addr + 192 * a, v);

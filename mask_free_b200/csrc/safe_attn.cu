@@ -733,8 +733,6 @@ safe_status launch_mx_linear(MxLinearParams& p, const void* X, const void* Xs, c
   const uint64_t ct = static_cast<uint64_t>(mx_tiles(d_in, kFmt)) * 64, rb = static_cast<uint64_t>(p.row_bytes);
   if (!encode_bytes_map(&p.x_map, X, false, rb, static_cast<uint64_t>(p.M), 128, 128) ||
       !encode_bytes_map(&p.w_map, W, false, rb, static_cast<uint64_t>(p.d_out), 128, 128) ||
-      !encode_bytes_map(&p.w96_map, W, false, rb, static_cast<uint64_t>(p.d_out), 128, 96) ||
-      !encode_bytes_map(&p.w32_map, W, false, rb, static_cast<uint64_t>(p.d_out), 128, 32) ||
       !encode_bytes_map(&p.xs_map, Xs, true, ct, static_cast<uint64_t>((p.M + 127LL) / 128), words, 1) ||
       !encode_bytes_map(&p.ws_map, Ws, true, ct, static_cast<uint64_t>((p.d_out + 127) / 128), words, 2))
     return SAFE_ERR_CUDA;
