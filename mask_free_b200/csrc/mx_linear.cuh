@@ -13,13 +13,19 @@
 //   scale A  of the CTA's own rows (one scale tile for each 4 scales of a row)
 //   scale B  of all 256 W rows, in both CTAs
 // Scales travel shared memory -> TMEM by tcgen05.cp (32 lanes x 16 B, copied
-// to all four lane quarters) right before the MMAs that use them; copies and
-// MMAs of one thread run in order, so one scale buffer serves every stage.
-// TMEM (512 columns): the last 64 hold the scales; the two accumulators of
-// 256 columns (tile i uses i & 1) overlap in 64 columns in the middle, the last
+// to all four lane quarters) right before the MMAs that use them. A copy is
+// ordered before the MMAs behind it; that it stays behind the MMAs in front,
+// whose scales it would overwrite, nothing says. So stages take two scale
+// buffers in turn, and a warp of its own keeps a stage from the issuing
+// warp until the MMAs two stages back are complete: it holds the second of the
+// two arrivals that the stage's barrier counts. (With one buffer and no wait 303
+// us, so 304: nvfp4 51200 x 2304 x 6912; with the wait in the issuing warp 344,
+// whatever stage it waits for.)
+// TMEM (512 columns): the last 96 hold the scales; the two accumulators of
+// 256 columns (tile i uses i & 1) overlap in 96 columns in the middle, the last
 // of accumulator 0 and the first of 1. A tile's first MMA waits until the
-// epilogue has read these from the tile before, which it does first of all;
-// the other 192 columns are read while the next tile is multiplied.
+// epilogue has read these from the tile before (with the 32 columns that its
+// warps read beside them); the others are read while the next tile is multiplied.
 // Every MMA of a tile has the same shape and accumulator: consecutive ones of one
 // thread are ordered under that condition only (a form whose first and last
 // stages did the shared columns apart, to hide that wait, added to them in two
@@ -28,16 +34,14 @@
 // 51200 x 2304 x 6912 336 and 328 us against 301).
 //
 // What bounds it: a stage is 34 - 38 KB into shared memory and as much out of
-// it for 512 cycles of MMA, and 1000 W. A call by itself (PFLOP/s; 51200 rows at
-// d_in = 2304, 12800 at 9216, d_out 6912): nvfp4 5.2 and 6.2, mxfp4 5.6 and 6.6,
-// mxfp8 3.1 and 2.9, with clocks down to 1.45 and 1.25 GHz; calls back to
-// back, when power sets the clock: nvfp4 3.9 and 4.9, mxfp8 2.3 and 2.25.
-// Measured on the way (nvfp4, d_in 2304 / 9216): tiles of 192 columns with
-// accumulators apart 4.2 / 4.9; accumulators that overlap without the split
-// 4.6 / 5.6 (the tensor core idles 1100 cycles at each tile); the output
-// through shared memory and tiled stores, which compete with the operands,
-// 4.9 / 5.8; a release instead of a relaxed arrival for the accumulator
-// 4.8 / 6.1.
+// it for 512 cycles of MMA, and 1000 W. A call by itself after an L2 flush
+// (PFLOP/s; 51200 rows at d_in = 2304, 12800 at 9216, d_out 6912): nvfp4 5.4 and
+// 6.3, mxfp4 5.6 and 6.6, mxfp8 3.0 and 2.9; 60 calls back to back: nvfp4 4.9
+// and 6.0, mxfp4 5.0 and 6.3, mxfp8 2.8 and 2.7. Measured on the way, each at its
+// time (nvfp4): tiles of 192 columns with accumulators apart 4.2 / 4.9; the
+// output through shared memory and tiled stores, which compete with the
+// operands, 4.9 / 5.8 against 5.2 / 6.2; a release instead of a relaxed arrival
+// for the accumulator 4.8 / 6.1.
 #pragma once
 
 #include "linear.cuh"
@@ -248,7 +252,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   uint8_t* sSA = sB + ST * kMxBBytes;
   uint8_t* sSB = sSA + ST * kSfA;
   float* sBias = reinterpret_cast<float*>(sSB + ST * kSfB);       // [16 epilogue warps][64]
-  uint64_t* full = reinterpret_cast<uint64_t*>(sBias + 16 * 64);  // [ST] both CTAs' stage loaded (rank 0)
+  // [ST] both CTAs' stage loaded, and the MMAs two stages back complete (rank 0)
+  uint64_t* full = reinterpret_cast<uint64_t*>(sBias + 16 * 64);
   uint64_t* empty = full + ST;                                     // [ST] stage consumed
   uint64_t* acc_full = empty + ST;                                 // [2] accumulator complete
   uint64_t* acc_empty = acc_full + 2;                              // [2] accumulator read back (rank 0)
@@ -267,14 +272,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < ST; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);
       mbar_init(&empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&acc_full[a], 1);
-      mbar_init(&acc_empty[a], 24);  // the epilogue warps of both CTAs that read its own columns
+      mbar_init(&acc_empty[a], 16);  // the epilogue warps of both CTAs that read its own columns
     }
-    mbar_init(sh_empty, 8);  // the epilogue warps that read them
+    mbar_init(sh_empty, 16);  // the epilogue warps that read them
     mbar_init(drain, 1);
     fence_mbar_init();
   }
@@ -345,7 +350,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       }
     }
     if ((!ok || abort_flag) && lane == 0 && rank == 0) {
-      // let every copy of the pair land before the CTAs exit
+      // let every copy of the pair land before the CTAs exit (a stage that its
+      // second arrival will not reach any more is given the wait's time, 200 ms)
       for (int g = issued - ST < 0 ? 0 : issued - ST; g < issued; ++g) mbar_wait_drain(&full[g % ST], (g / ST) & 1);
     }
   } else if (warp == 1 && rank == 0) {
@@ -362,7 +368,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     const int last_steps = (p.row_bytes - 128 * (nk - 1) + 31) / 32;  // 32-byte steps of the last stage
     int s = 0;
     uint32_t round = 0;
-    constexpr uint32_t sfa = tbase + 448, sfb = sfa + 16;
+    // the stage's scales: of X, of W; buffers of 48 columns taken in turn
+    constexpr uint32_t sfa0 = tbase + 416, sfb0 = sfa0 + 4 * KT;
+    uint32_t sfa = sfa0, sfb = sfb0;
     bool ok = true;
     for (int i = 0; i < n_local && ok; ++i) {
       const int a = i & 1;
@@ -371,7 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t tacc = tbase + 192 * a;
+      const uint32_t tacc = tbase + 160 * a;
       const int piece = pair + i * n_pairs - p.whole;
       const int n = piece < 0 ? nk : p.piece_n[piece];
       const int last = piece < 0 || p.piece_k0[piece] + n == nk ? last_steps : 4;
@@ -420,6 +428,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         }
         // both CTAs' stage may be refilled once these copies and MMAs have read it
         umma_pair_commit_both_if(leader, smem_u32(&empty[s]));
+        sfa = 2 * sfa0 + 48 - sfa;
+        sfb = 2 * sfb0 + 48 - sfb;
         if (++s == ST) {
           s = 0;
           round ^= 1u;
@@ -432,6 +442,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       umma_pair_commit_if(leader, cluster_addr(drain, 0));
       if (leader) mbar_wait_drain(drain, 0);
       __syncwarp();
+    }
+  } else if (warp == 2 && rank == 0) {
+    // ------------------------------------------------------------ the scale buffers' turns (even CTA)
+    int stages = 0;
+    for (int i = 0; i < n_local; ++i) {
+      const int piece = pair + i * n_pairs - p.whole;
+      stages += piece < 0 ? nk : p.piece_n[piece];
+    }
+    // Stage g may overwrite the scales of stage g - 2. (A slot is not issued again
+    // before its arrival here, so its barrier cannot run ahead of this warp.)
+    int s = 0, back = ST - 2;
+    uint32_t parity = 1;
+    for (int g = 0; g < stages; ++g) {
+      if (g >= 2 && !warp_wait_short(&empty[back], parity, &abort_flag)) break;
+      tc_fence_after();
+      tc_fence_before();
+      if (lane == 0) mbar_arrive(&full[s]);
+      if (++s == ST) s = 0;
+      if (++back == ST) {
+        back = 0;
+        parity ^= 1u;
+      }
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue (both CTAs)
@@ -460,12 +492,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       __syncwarp();  // the last tile's bias has been read
       bias2[lane] = next;
       next = load_bias(i + 1);
-      const bool sh = e == (a ? 0 : 3);
+      const bool sh = (e >> 1) == (a ^ 1);  // these warps' columns reach into the shared ones
       if (!warp_wait_short(&acc_full[a], (i >> 1) & 1, &abort_flag)) break;
       tc_fence_after();
       uint32_t v[64];
-      tmem_ld32(lane_addr + 192 * a, v);
-      tmem_ld32(lane_addr + 192 * a + 32, v + 32);
+      tmem_ld32(lane_addr + 160 * a, v);
+      tmem_ld32(lane_addr + 160 * a + 32, v + 32);
       tmem_ld_wait32(v);
       tmem_ld_wait32(v + 32);
       tc_fence_before();
