@@ -68,3 +68,52 @@ def test_update_in_place_of_long_lists(k):
     assert counted(S, N)[0].all() and not counted(S, N)[1, k - 1] and not counted(S, N)[2, 701:].any()
     for dtype, D, quant in ((bf16, 32, "mxfp8"), (f32, 40, None)):
         update_check(S, N, D, dtype, quant, 11)
+
+
+# ---------------------------------------------------------------- every form of the norm, at both ends of its widths
+def norm_check(dtype, N, D, S, seed):
+    w = 1 + 0.2 * randn((D,), seed)
+    x, r = randn((1, len(S[0]) if S is not None else N, D), seed + 1, dtype), 2 * randn((1, N, D), seed + 2, dtype)
+    href, yref = O.rms_norm(to64(x), to64(w), to64(r), S)
+    y, h = ops.rms_norm(dev(x), dev(w), dev(r), dev(S), x_compact=S is not None)
+    assert np.all(np.abs(to64(y) - yref) <= half_step(dtype, yref) * (1 + 1e-6) + norm_tol(yref, D))
+    assert np.all(np.abs(to64(h) - href) <= half_step(dtype, href) * (1 + 1e-6) + np.abs(href) * U)
+    if S is None:  # without the residual and the weight
+        _, yref = O.rms_norm(to64(x))
+        y = ops.rms_norm(dev(x))
+        assert np.all(np.abs(to64(y) - yref) <= half_step(dtype, yref) * (1 + 1e-6) + norm_tol(yref, D))
+    assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [bf16, f16, f32])
+@pytest.mark.parametrize("D", [8, 64, 72, 256, 264, 512, 520, 1024, 1032, 1536, 1544, 2048, 2056, 2304, 2312, 3064, 3080, 4096,
+                               4104, 7168, 7176, 10240, 10248, 20480, 20488, 40960, 40968])
+def test_norm_of_widths_in_units_of_8(dtype, D):
+    for N in (5, 37) if D < 4096 else (5,):
+        norm_check(dtype, N, D, None, D)
+    norm_check(dtype, 9, D, np.array([[0, 3, 4, 8]], dtype=np.int32), D)
+
+
+@pytest.mark.parametrize("dtype", [bf16, f16, f32])
+@pytest.mark.parametrize("D", [1, 7, 9, 63, 65, 249, 250, 319, 321, 505, 507, 1009, 1019, 1279, 1281, 1521, 1531, 2001, 2033, 2043,
+                               2289, 2299, 2303, 2559, 2561, 3057, 3059, 4081, 4083, 7153, 7155, 10225, 10227, 20465, 20467])
+def test_norm_of_other_widths(dtype, D):
+    # without S by shifted units, with S one by one; rows that share units with both neighbours
+    norm_check(dtype, 11, D, None, D)
+    norm_check(dtype, 9, D, np.array([[0, 3, 4, 8]], dtype=np.int32), D)
+
+
+@pytest.mark.parametrize("dtype", [bf16, f16, f32])
+@pytest.mark.parametrize("D", [32, 64, 256, 288, 512, 544, 1024, 1056, 1536, 1568, 2048, 2080, 2304, 2336, 3040, 3104, 4096, 4128,
+                               7168, 7200, 10240, 10272, 20480, 20512, 40960])
+def test_norm_in_8_bits_of_every_width(dtype, D):
+    N = 133 if D < 4096 else 5  # more than one tile of scales
+    x, r, w = randn((1, N, D), D, dtype), randn((1, N, D), D + 1, dtype), 1 + 0.2 * randn((D,), D + 2)
+    x[..., ::17] *= 8
+    for S in (None, np.arange(1, N, 2, dtype=np.int32)[None]):
+        xs = x if S is None else x[:, :S.shape[1]].contiguous()
+        href, yref = O.rms_norm(to64(xs), to64(w), to64(r), S)
+        y, h = ops.rms_norm(dev(xs), dev(w), dev(r), dev(S), x_compact=S is not None, quant="mxfp8")
+        assert np.all(np.abs(to64(h) - href) <= half_step(dtype, href) * (1 + 1e-6) + np.abs(href) * U)
+        check_mxfp8(y, yref, (D / 2 + 8) * U)
+    assert ops.device_status() == 0
