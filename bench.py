@@ -10,6 +10,7 @@ between steps.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
     python bench.py --only KERNEL [--workload W] [--launches L]   (one kernel, for profilers)
+    python bench.py --operators [both]                            (the row-wise operators' table)
 
 Prints one JSON line (rank 0). `value` is attention TFLOP/s of the step:
 algorithmic FLOPs of dense self-attention (4 B H N^2 d) plus SRSU
@@ -631,6 +632,88 @@ def run_only(kernel: str, workload: str, launches: int):
     print(json.dumps({"only": kernel, "workload": workload, "launches": launches, "status": "ok"}))
 
 
+MX_RATE = {"mxfp8": 2, "mxfp4": 4, "nvfp4": 4}  # nominal rate of a format's products over bf16's
+# layers whose kernel is timed by itself: rows, d_in, d_out, activation
+MX_LAYERS = ((51200, 2304, 6912, "none"), (12800, 2304, 9216, "gelu_tanh"), (12800, 9216, 6912, "none"),
+             (2458, 9216, 2304, "none"))
+
+
+def operator_limit(case, work, pk):
+    """Microseconds for a pass's bytes at the measured copy rate, or for a
+    layer's products at the measured bf16 rate times the format's, whichever is
+    longer. Not a lower bound where inputs stay in L2 between passes."""
+    us = work["bytes"] / pk["hbm"] / 1e3
+    if case["op"] == "linear":
+        us = max(us, work["flops"] / (pk["bf16"] * MX_RATE[case["fmt"]]) / 1e6)
+    return us
+
+
+def time_passes(fn, seconds=0.5):
+    """(us a pass, passes) of eager passes back to back for about `seconds`, the
+    host's work included."""
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+
+    def batch(n):
+        torch.cuda.synchronize()
+        ev[0].record()
+        for _ in range(n):
+            fn()
+        ev[1].record()
+        torch.cuda.synchronize()
+        return ev[0].elapsed_time(ev[1]) * 1e3 / n
+
+    batch(3)
+    n = max(5, int(seconds * 1e6 / batch(5)))
+    return batch(n), n
+
+
+def time_one_cool(fn):
+    """Device us of a single call after an L2 flush, on a GPU that has idled for a
+    second (behind seconds at the power limit the clock stays low)."""
+    torch.cuda.synchronize()
+    time.sleep(1.0)
+    return time_flushed(fn) * 1e3
+
+
+def run_operators(which):
+    """One JSON line for each measured case of the row-wise operators
+    (perf/operators.py) and for each of MX_LAYERS: us a pass back to back,
+    device us of a single pass (time_one_cool), and with `which` "both" the
+    plain forms' pass; then one with the clocks of the whole run."""
+    from mask_free_b200 import ops
+    from perf import operators as P
+    pk, dev = peaks(), torch.device("cuda", torch.cuda.current_device())
+    r1 = lambda v: round(v, 1)
+    with ClockSampler(dev.index) as clk:
+        for case in P.listed():
+            P.own = True
+            state = P.prepare(case, 1)
+            one = time_one_cool(lambda: P.run(state))
+            us, n = time_passes(lambda: P.run(state))
+            line = {"case": case["name"], "limit_us": round(operator_limit(case, P.work(case), pk), 3), "pass_us": r1(us),
+                    "passes": n, "device_us": r1(one)}
+            P.own = False
+            if which == "both":
+                line["plain_us"] = r1(time_passes(lambda: P.run(state), 0.1)[0])
+            print(json.dumps(line), flush=True)
+            del state
+            torch.cuda.empty_cache()
+        gen = torch.Generator(device=dev).manual_seed(1)
+        for fmt in MX_RATE:
+            for M, d_in, d_out, act in MX_LAYERS:
+                X, W = (ops.mx_quantize(torch.randn((n, d_in), generator=gen, device=dev), fmt,
+                                        scale=0.003 if fmt == "nvfp4" else 1.0) for n in (M, d_out))
+                out = torch.empty((M, d_out), dtype=torch.bfloat16, device=dev)
+                bias = torch.randn(d_out, generator=gen, device=dev)
+                fn = lambda: ops.mx_linear(X, W, bias, act, out=out)
+                one, (us, n) = time_one_cool(fn), time_passes(fn, 2.0)
+                flop = 2.0 * M * d_in * d_out
+                print(json.dumps({"layer": f"{fmt} {M} x {d_in} x {d_out} {act}", "device_us": r1(one),
+                                  "pflops": round(flop / one / 1e9, 2), "back_to_back_us": r1(us), "calls": n,
+                                  "pflops_back_to_back": round(flop / us / 1e9, 2)}), flush=True)
+    print(json.dumps({"clocks": clk.summary(), "peaks": pk["source"]}), flush=True)
+
+
 def host_info():
     """Host cores and CPU model of the box the oracle runs on."""
     model = None
@@ -762,7 +845,12 @@ def main():
                     help="launch one kernel and nothing else (for profilers); no JSON bench line")
     ap.add_argument("--workload", default="n4096", choices=sorted(synth.WORKLOADS), help="workload of --only")
     ap.add_argument("--launches", type=int, default=3, help="launches of --only")
+    ap.add_argument("--operators", default=None, nargs="?", const="kernels", choices=["kernels", "both"],
+                    help="time the row-wise operators' cases and nothing else (both: their plain forms too)")
     args = ap.parse_args()
+    if args.operators is not None:
+        run_operators(args.operators)
+        return
     if args.only is not None:
         run_only(args.only, args.workload, args.launches)
         return
