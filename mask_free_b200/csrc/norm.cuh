@@ -84,8 +84,9 @@ __device__ __forceinline__ bool norm_rows(const NormParams& p, int row, bool fla
   return ok;
 }
 
-// Whether a row of norm_rows is in order; taken behind its loads, which need not
-// wait for the marks, and ahead of everything that writes.
+// Whether a row is in order; taken behind the loads, which need not wait for the
+// marks, and ahead of everything that writes. Rows of a bad index take it too: the
+// zeros of their y must not be in memory before their mark.
 __device__ __forceinline__ bool norm_in_order(const NormParams& p, int row, bool flag) {
   if (p.mark == nullptr) return true;
   pdl_wait();
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(TPR <= 32 ? 128 : TPR) rms_norm_kernel(const N
     }
   }
   // (kNormShift: without S)
-  const bool ok = kMode == kNormShift ? found : found && norm_in_order(p, row, t == 0);
+  const bool ok = kMode == kNormShift ? found : live && norm_in_order(p, row, t == 0) && found;
   const bool h_write = kMode == kNormShift ? h_found : h_found && (ok || !p.h_full);
   float ss = 0.f;
   if constexpr (VEC == 8) {
@@ -305,7 +306,8 @@ __global__ void __launch_bounds__(512) rms_norm_long_kernel(const NormParams p) 
   __shared__ float part[16];
   const int row = static_cast<int>(blockIdx.x);
   int xr, rr, hr;
-  const bool ok = norm_rows(p, row, threadIdx.x == 0, xr, rr, hr) && norm_in_order(p, row, threadIdx.x == 0);
+  const bool found = norm_rows(p, row, threadIdx.x == 0, xr, rr, hr);
+  const bool ok = norm_in_order(p, row, threadIdx.x == 0) && found;
   const T* x = static_cast<const T*>(p.x) + static_cast<size_t>(ok ? xr : 0) * p.D;
   const T* res = p.res != nullptr ? static_cast<const T*>(p.res) + static_cast<size_t>(ok ? rr : 0) * p.D : nullptr;
   T* h = p.h != nullptr ? static_cast<T*>(p.h) + static_cast<size_t>(ok ? hr : p.h_full ? 0 : row) * p.D : nullptr;

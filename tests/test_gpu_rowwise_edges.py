@@ -117,3 +117,20 @@ def test_norm_in_8_bits_of_every_width(dtype, D):
         assert np.all(np.abs(to64(h) - href) <= half_step(dtype, href) * (1 + 1e-6) + np.abs(href) * U)
         check_mxfp8(y, yref, (D / 2 + 8) * U)
     assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,D,quant", [(bf16, 8, None), (bf16, 2304, None), (f32, 63, None), (bf16, 41000, None),
+                                           (bf16, 32, "mxfp8"), (f16, 2304, "mxfp8")])
+def test_update_in_place_of_bad_rows_only(dtype, D, quant):
+    # rows of no token: their y is zeros, whichever of the call's two kernels comes to it last
+    B, N, k = (2, 30000, 25000) if D < 64 else (2, 3000, 2600) if D < 4096 else (2, 400, 300)
+    S = torch.full((B, k), -1, dtype=torch.int32, device=DEV)
+    S[1, ::3] = N
+    x, stream = (torch.ones((B, n, D), dtype=dtype, device=DEV) for n in (k, N))
+    for _ in range(10):
+        y, _ = ops.rms_norm(x, None, stream, S, x_compact=True, quant=quant, update=True)
+        v = y if quant is None else ops.mx_dequantize(y, f32)
+        assert not v.any() and ops.device_status() == FLAG
+        if quant is not None:
+            assert not y.data.view(torch.uint8).any() and not y.scales.any()
+    assert bool((stream == 1).all())
