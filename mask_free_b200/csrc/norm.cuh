@@ -36,36 +36,44 @@ struct NormParams {
 // row, so a row counts only where its index lies above every earlier one of its
 // sample: at most one row of an index does. This kernel runs ahead of the norm and
 // leaves a byte for each row where the norm will write that row's y (or q), which the
-// norm reads first. A CTA marks 1024 rows of a sample, after the largest of all
-// the indices in front of them: reads that grow with the square of the rows,
-// but by 1 / 1024 (25600 rows: 1.3 MB), and no CTA waits for another. Measured
-// (bf16, two samples, D = 2304, to 8 bits, with / without the update in place):
-// 6400 rows each 50 / 45 us, 1229 each 19.5 / 16.4; 64 rows of one sample 9.2 / 8.2.
-__global__ void __launch_bounds__(1024) norm_order_kernel(const int32_t* S, int R, uint8_t* mark, size_t pitch) {
-  __shared__ int before[32], own[32];
+// norm reads first. A CTA marks `per` rows of a sample (a multiple of 1024), after
+// the largest of all the indices in front of them, so that no CTA waits for
+// another: CTAs times rows reads in all, and so 128 CTAs at most (25600 rows in 25
+// CTAs: 1.3 MB). Measured (bf16, two samples, D = 2304, to 8 bits, with / without the
+// update in place): 6400 rows each 50 / 45 us, 1229 each 19.5 / 16.4; 64 rows of one
+// sample 9.2 / 8.2.
+constexpr int kNormOrderCtas = 128;
+__global__ void __launch_bounds__(1024)
+    norm_order_kernel(const int32_t* S, uint32_t R, uint32_t per, uint8_t* mark, size_t pitch) {
+  __shared__ int before[32], own[2][32];
   pdl_launch_dependents();  // the norm may start: it waits for the marks only
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = static_cast<int>(blockIdx.x) * 1024;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t first = blockIdx.x * per, end = R - first < per ? R : first + per;
   S += static_cast<size_t>(blockIdx.y) * R;
-  int top = -1;
-  for (int i = threadIdx.x; i < first; i += 1024) top = max(top, S[i]);
-  const bool live = static_cast<int>(threadIdx.x) < R - first;
-  const int idx = live ? S[first + threadIdx.x] : -1;
-  int upto = idx;  // the largest of the warp's indices up to this one
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto = max(upto, v);
-  }
+  mark += static_cast<size_t>(blockIdx.y) * R * pitch;
+  int top = -1;  // the largest index in front of the next 1024 rows
+  for (uint32_t i = threadIdx.x; i < first; i += 1024) top = max(top, S[i]);
   top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 31) {
-    before[warp] = top;
-    own[warp] = upto;
-  }
+  if (lane == 0) before[warp] = top;
   __syncthreads();
-  top = __reduce_max_sync(0xffffffffu, max(before[lane], lane < warp ? own[lane] : -1));
-  const int left = __shfl_up_sync(0xffffffffu, upto, 1);
-  if (lane > 0) top = max(top, left);
-  if (live) mark[(static_cast<size_t>(blockIdx.y) * R + first + threadIdx.x) * pitch] = idx <= top;
+  top = __reduce_max_sync(0xffffffffu, before[lane]);
+  for (uint32_t at = first, turn = 0; at < end; at += 1024, turn ^= 1) {
+    const uint32_t r = at + threadIdx.x;
+    const int idx = r < end ? S[r] : -1;
+    int upto = idx;  // the largest of the warp's indices up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto = max(upto, v);
+    }
+    if (lane == 31) own[turn][warp] = upto;
+    __syncthreads();
+    const int other = own[turn][lane], left = __shfl_up_sync(0xffffffffu, upto, 1);
+    int front = max(top, __reduce_max_sync(0xffffffffu, lane < warp ? other : -1));
+    if (lane > 0) front = max(front, left);
+    if (r < end) mark[r * pitch] = idx <= front;
+    top = max(top, __reduce_max_sync(0xffffffffu, other));
+  }
 }
 
 // Rows of a tensor for output row `row`; false: a bad index (flagged), the

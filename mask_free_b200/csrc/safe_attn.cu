@@ -1219,8 +1219,10 @@ safe_status safe_rms_norm(const void* x, int x_full, const void* res, const int3
     uint8_t* mark = static_cast<uint8_t*>(y != nullptr ? y : q);
     p.mark = mark;
     p.mark_pitch = static_cast<size_t>(D) * (y != nullptr ? e : 1);
-    const dim3 grid(static_cast<unsigned>((R + 1023LL) / 1024), static_cast<unsigned>(B));
-    norm_order_kernel<<<grid, 1024, 0, as_stream(stream)>>>(S, R, mark, p.mark_pitch);
+    const unsigned tiles = (static_cast<unsigned>(R) + 1023u) / 1024u;
+    const unsigned per = (tiles + kNormOrderCtas - 1) / kNormOrderCtas, ctas = (tiles + per - 1) / per;
+    norm_order_kernel<<<dim3(ctas, static_cast<unsigned>(B)), 1024, 0, as_stream(stream)>>>(
+        S, static_cast<uint32_t>(R), 1024 * per, mark, p.mark_pitch);
     const safe_status st = launch_status();
     if (st != SAFE_OK) return st;
   }

@@ -134,3 +134,26 @@ def test_update_in_place_of_bad_rows_only(dtype, D, quant):
         if quant is not None:
             assert not y.data.view(torch.uint8).any() and not y.scales.any()
     assert bool((stream == 1).all())
+
+
+@pytest.mark.parametrize("k", [128 * 1024, 128 * 1024 + 1, 300007])
+def test_update_in_place_of_very_long_lists(k):
+    # more than 1024 rows to a CTA of the marks; an index again from other runs, rows behind a large one
+    N, D = 300500, 8
+    S = rows(2, N, k, k)
+    again = [(1023, 5), (1024, 1023), (3000, 3000 - 1), (k - 1, k // 2), (k // 2 + 7, 0)]
+    for at, of in again:
+        S[0, at] = S[0, of]
+    S[1, k - 3000] = N - 1
+    ok = counted(S, N)
+    assert not any(ok[0, at] for at, _ in again) and not ok[1, k - 2999:].any() and ok[1, :k - 2999].all()
+    x, r = randn((2, k, D), 1, bf16).to(DEV), randn((2, N, D), 2, bf16).to(DEV)
+    stream = r.clone()
+    y, _ = ops.rms_norm(x, None, stream, dev(S), x_compact=True, update=True)
+    assert ops.device_status() == FLAG
+    y0, h0 = ops.rms_norm(x, None, r, dev(S), x_compact=True)  # apart, an index may come again
+    okd = torch.from_numpy(ok).to(DEV)
+    want = r.clone()
+    for b in range(2):
+        want[b, torch.from_numpy(S[b][ok[b]]).long().to(DEV)] = h0[b][okd[b]]
+    assert torch.equal(stream, want) and torch.equal(y, torch.where(okd[..., None], y0, torch.zeros_like(y0)))
