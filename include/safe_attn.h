@@ -378,7 +378,8 @@ safe_status safe_gather_linear(const void* X, const int32_t* S, int k, const voi
  * them with D a multiple of 8 is faster, and with q it is required, with D a
  * multiple of 32 and at most 40960. Outputs may not overlap each other or an
  * input, except that without S h and y may each be x or res themselves. All
- * arithmetic is fp32: the norm takes the unrounded sum h.
+ * arithmetic is fp32: the norm takes the unrounded sum h, and a row whose sum of
+ * squares passes fp32's range (magnitudes from about 1e18 on) has a y of zeros.
  */
 safe_status safe_rms_norm(const void* x, int x_full, const void* res, const int32_t* S, int k, const float* w,
                           float eps, void* h, int h_full, void* y, void* q, void* q_scales, int dtype, int B, int N,
@@ -473,7 +474,8 @@ safe_status safe_mx_dequantize(const void* data, const void* scales, int fmt, fl
  *        safe_gather_linear (0 = none, 1 = tanh-GELU).
  *  Y     device bf16 [rows, d_out] (written; apart from the operands and bias).
  *  ws    device workspace of safe_mx_linear_workspace_bytes bytes (32-byte
- *        aligned; caller-owned, contents undefined after the call) or NULL:
+ *        aligned; caller-owned, contents undefined after the call, not to be
+ *        shared by calls that may run at the same time) or NULL:
  *        with it, the tiles of the last, partial wave of CTAs are computed in
  *        pieces along d_in and added by a second kernel (fp32, in a fixed
  *        order). The size is 0 where that does not pay off; without it, or

@@ -35,10 +35,10 @@
 //
 // What bounds it: a stage is 34 - 38 KB into shared memory and as much out of
 // it for 512 cycles of MMA, and 1000 W. A call by itself after an L2 flush
-// (PFLOP/s; 51200 rows at d_in = 2304, 12800 at 9216, d_out 6912): nvfp4 5.4 and
-// 6.3, mxfp4 5.6 and 6.6, mxfp8 3.0 and 2.9; 60 calls back to back: nvfp4 4.9
-// and 6.0, mxfp4 5.0 and 6.3, mxfp8 2.8 and 2.7. Measured on the way, each at its
-// time (nvfp4): tiles of 192 columns with accumulators apart 4.2 / 4.9; the
+// (PFLOP/s; 51200 rows at d_in = 2304, 12800 at 9216, d_out 6912): nvfp4 5.1 - 5.4
+// and 6.2, mxfp4 5.5 and 6.7, mxfp8 2.9 and 2.7; calls back to back for two
+// seconds, when power sets the clock: nvfp4 4.1 and 5.0, mxfp4 4.3 and 5.4, mxfp8
+// 2.3 and 2.2. Measured on the way, each at its time (nvfp4): tiles of 192 columns with accumulators apart 4.2 / 4.9; the
 // output through shared memory and tiled stores, which compete with the
 // operands, 4.9 / 5.8 against 5.2 / 6.2; a release instead of a relaxed arrival
 // for the accumulator 4.8 / 6.1.
@@ -189,7 +189,8 @@ __host__ __device__ constexpr int mx_linear_smem(int fmt) {
 // arithmetic: 11 instructions with the rounding, 4 of them the exp unit's. (One
 // reciprocal for both, of the product, takes one of those less, but 19 with
 // what keeps the product finite and a NaN to itself: nvfp4, 12800 x 2304 x 9216,
-// back to back 158 us, this 149, without an activation 137.)
+// back to back 158 us at that step, this 149. Now 125, without an activation 114,
+// in 60 calls back to back.)
 __device__ __forceinline__ uint64_t gelu_tanh_2(uint64_t x) {
   const uint64_t c2 = f2_pack(-0.10294324f, -0.10294324f), c1 = f2_pack(-2.3022082f, -2.3022082f);
   float t0, t1, a, b;
@@ -300,8 +301,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   // dependent launch); nothing is read or written before every thread has waited
   // for that kernel. The signal comes after the allocation: a kernel behind that
   // allocates columns can then take none that this one still needs. Layers back to
-  // back, without it and with it: mxfp8 4096 x 6912 x 2304 51.6 -> 48.3 us,
-  // 1024 x 2304 x 2304 18.5 -> 15.2, mxfp4 16 x 2304 x 2304 10.7 -> 10.3.
+  // back, without it and with it: mxfp8 4096 x 2304 x 6912 56 -> 52 us,
+  // 1024 x 2304 x 2304 18.4 -> 14.8, mxfp4 16 x 2304 x 2304 11.1 -> 10.5.
   pdl_launch_dependents();
   pdl_wait();
 

@@ -694,8 +694,8 @@ int resident_pairs(int threads, int smem) {
 // The second launch costs what 12 stages do, the pieces' way through memory 28
 // for 64 full pieces, so a split has to save more. Measured with / without
 // (mxfp8, d_in 9216, d_out 2304): 2458 rows 49 / 57 us (90 tiles on 74 pairs, the
-// last 16 in 4 pieces), 300 rows 27 / 33, 2 rows 18 / 29; where it would not
-// pay: 1000 rows (halves) 35 / 33, nvfp4 (half the stages) 2458 rows 35 / 34.
+// last 16 in 4 pieces), 300 rows 25 / 33, 2 rows 16 / 29; where it would not
+// pay, at an earlier step: 1000 rows (halves) 35 / 33, nvfp4 (half the stages) 2458 rows 35 / 34.
 struct MxPlan {
   int pairs, n_tiles, rest, whole, split;
   int64_t units;

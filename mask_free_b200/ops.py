@@ -978,7 +978,8 @@ def mx_linear(X: MxTensor, W: MxTensor, bias=None, act="none", out=None, ws=None
     row-selective block), W [d_out, d_in], both of one format; bias [d_out]
     fp32, act "none" or "gelu_tanh". Returns bf16 [..., d_out].
     ws: the workspace for splitting the last wave's tiles along d_in (a fresh
-    one when None; False: every tile whole)."""
+    one when None; False: every tile whole; not shared by calls that may run at
+    the same time)."""
     if not isinstance(X, MxTensor) or not isinstance(W, MxTensor):
         raise ValueError("X and W must be MxTensors")
     fmt, x, w = X._fmt, X._data, W._data
