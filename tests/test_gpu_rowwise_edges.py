@@ -157,3 +157,61 @@ def test_update_in_place_of_very_long_lists(k):
     for b in range(2):
         want[b, torch.from_numpy(S[b][ok[b]]).long().to(DEV)] = h0[b][okd[b]]
     assert torch.equal(stream, want) and torch.equal(y, torch.where(okd[..., None], y0, torch.zeros_like(y0)))
+
+
+def test_norm_past_the_range_of_its_squares():
+    # finite rows whose sum of squares is infinite in fp32: zeros, and their sums h as they are
+    x = torch.full((1, 3, 64), 1e19, dtype=f32, device=DEV)
+    x[0, 1] = 3.0
+    y, h = ops.rms_norm(x, None, torch.zeros_like(x))
+    assert not y[0, 0].any() and not y[0, 2].any() and torch.equal(h, x)
+    assert torch.allclose(y[0, 1], torch.ones(64, device=DEV), rtol=1e-6)
+
+
+@pytest.mark.parametrize("quant", [None, "mxfp8"])
+@pytest.mark.parametrize("D,k", [(64, 90), (2304, 1500)])
+def test_update_in_place_captured_and_on_two_streams(D, k, quant):
+    # the marks and the norm behind them: replayed on other lists and inputs, full x, two calls at once
+    B, N = 2, 1600
+    w = (1 + 0.2 * randn((D,), 1)).to(DEV)
+    lists = [rows(B, N, k, i) for i in range(3)]
+    lists[1][0, k // 2] = lists[1][0, 1]  # an index again
+    lists[2][1, 3], lists[2][1, 7] = -1, N
+    cases = [(dev(S), randn((B, N, D), 10 + i, bf16).to(DEV), randn((B, N, D), 20 + i, bf16).to(DEV)) for i, S in enumerate(lists)]
+
+    def call(S, x, stream):
+        y, _ = ops.rms_norm(x, w, stream, S, quant=quant, update=True)
+        return y if quant is None else ops.mx_dequantize(y)
+
+    want = []
+    for (S, x, r), host in zip(cases, lists):
+        stream, ok = r.clone(), torch.from_numpy(counted(host, N)).to(DEV)
+        want.append((call(S, x, stream), stream))
+        y0, h0 = ops.rms_norm(x, w, r, S, quant=quant)  # apart
+        y0 = y0 if quant is None else ops.mx_dequantize(y0)
+        assert torch.equal(want[-1][0], torch.where(ok[..., None], y0, torch.zeros_like(y0)))
+        full = r.clone()
+        for b in range(B):
+            full[b, S[b][ok[b]].long()] = h0[b][ok[b]]
+        assert torch.equal(stream, full)
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for (S, x, r), st in zip(cases, streams):
+            with torch.cuda.stream(st):
+                stream = r.clone()
+                got.append((call(S, x, stream), stream))
+    torch.cuda.synchronize()
+    for i, (y, stream) in enumerate(got):
+        assert torch.equal(y, want[i % 2][0]) and torch.equal(stream, want[i % 2][1])
+    S, x, r = (t.clone() for t in cases[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = call(S, x, r)
+    for i in (1, 2, 0, 1):
+        for a, b in zip((S, x, r), cases[i]):
+            a.copy_(b)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i][0]) and torch.equal(r, want[i][1])
+    assert ops.device_status() == FLAG
